@@ -72,6 +72,7 @@ typedef enum llmint8_status {
 #define LLMINT8_DEV_TIMEOUT_EPILOGUE 0x4u
 #define LLMINT8_DEV_TIMEOUT_QUANT 0x8u
 #define LLMINT8_DEV_BAD_STORE 0x10u /* an epilogue store failed its self-check and was skipped */
+#define LLMINT8_DEV_BAD_PAGE 0x20u  /* a position's page was not in the table or the cache; it was left out */
 
 /* Human-readable name of a status code. Never NULL. */
 LLMINT8_API const char *llmint8_status_string(int status);
@@ -426,6 +427,144 @@ LLMINT8_API llmint8_status llmint8_quantize_rowwise_noalloc(const void *X_f16, i
  * LLMINT8_ERR_DEVICE when it is not, LLMINT8_ERR_CUDA if a CUDA call failed,
  * LLMINT8_ERR_INVALID_ARG for a NULL out. Allocates nothing. */
 LLMINT8_API llmint8_status llmint8_noalloc_read_status(int clear, uint32_t *out);
+
+/* 16-bit value types of the entry points below. */
+#define LLMINT8_TYPE_F16 0
+#define LLMINT8_TYPE_BF16 1
+
+/*
+ * The step before a linear in a transformer block, fused with the linear's
+ * row quantization: add the residual, take the root-mean-square norm, and
+ * quantize the result's rows ([Q], [M]). X, residual, weight and residual_out
+ * have the type `type`:
+ *   h[i,c] = X[i,c] + residual[i,c], rounded to `type` (h = X without residual)
+ *   y[i,c] = fp16( h[i,c] * weight[c] / sqrt(mean_c(h[i,:]^2) + eps) ), in fp32
+ * and codes, row_absmax and outlier_bitmap are exactly what
+ * llmint8_quantize_rowwise(y, threshold) gives.
+ *   X            (device) [rows x cols]; cols a multiple of 16
+ *   residual     (device, may be NULL) [rows x cols]
+ *   weight       (device) [cols]
+ *   residual_out (device, may be NULL) [rows x cols] out: h. May be X or
+ *                residual itself.
+ *   Y_f16        (device) fp16 [rows x cols] out: y, the X_f16 of
+ *                llmint8_matmul_codes. Required when t > 0, may be NULL
+ *                otherwise. Must not overlap any other argument.
+ *   codes, row_absmax, outlier_bitmap, threshold, workspace: as
+ *                llmint8_quantize_rowwise; workspace at least
+ *                llmint8_quantize_workspace_size(rows, cols) bytes.
+ * Errors as llmint8_quantize_rowwise; a bad type or an eps that is negative
+ * or not finite is LLMINT8_ERR_INVALID_ARG.
+ */
+LLMINT8_API llmint8_status llmint8_add_rmsnorm_quantize(const void *X, const void *residual, const void *weight,
+                                            int type, int64_t rows, int64_t cols, float eps, float threshold,
+                                            void *residual_out, void *Y_f16, int8_t *codes, float *row_absmax,
+                                            uint32_t *outlier_bitmap, void *workspace, size_t ws_bytes,
+                                            llmint8_stream_t stream);
+
+/* The values row codes stand for ([U]: CB * SCB / 127): out[i,c] =
+ * codes[i,c] * (row_absmax[i] / 127) in fp32, rounded to `type`. codes
+ * (device) int8 [rows x cols], row_absmax (device) fp32 [rows], out (device)
+ * [rows x cols]; cols a multiple of 16. No workspace. */
+LLMINT8_API llmint8_status llmint8_dequantize_rowwise(const int8_t *codes, const float *row_absmax, int64_t rows,
+                                          int64_t cols, int type, void *out, llmint8_stream_t stream);
+
+/*
+ * The paged int8 key/value cache. A page holds page_size tokens of every
+ * head; every (page, head) has one absmax for its keys and one for its
+ * values, the absmax quantization of [Q] over a block of tokens of one head:
+ *   value = code * (absmax / 127).
+ * Sequence b has seq_lens[b] tokens; position j lies in page
+ * page_table[b * table_stride + j / page_size], slot j % page_size. The calls
+ * work on packed rows: rows cu_rows[b] .. cu_rows[b+1] - 1 belong to sequence
+ * b and are its LAST positions, seq_lens[b] - n .. seq_lens[b] - 1 with
+ * n = cu_rows[b+1] - cu_rows[b] (rows whose position would be negative take
+ * no part). seq_lens therefore counts the rows of the call, those that
+ * llmint8_kv_append is writing included. Rows at and behind cu_rows[batch]
+ * belong to no sequence and are neither read nor written. All of these are
+ * device arrays, so that a captured graph can be replayed with other lengths.
+ *
+ * page_table entries past a sequence's pages are not read. A position whose
+ * page is not in the table (j / page_size >= table_width) or not in the cache
+ * (a number outside 0 .. pages - 1) is left out (not written, not read, no
+ * key of the attention), and LLMINT8_DEV_BAD_PAGE is set in the status word.
+ */
+typedef struct llmint8_kv_cache {
+    int8_t *k_codes, *v_codes;   /* (device) [pages x heads x page_size x head_dim], 16-byte aligned */
+    float *k_absmax, *v_absmax;  /* (device) [pages x heads] */
+    int64_t pages;
+    int32_t heads;               /* key/value heads */
+    int32_t page_size;           /* 16, 32, 64 or 128 */
+    int32_t head_dim;            /* 64 or 128 */
+    int32_t batch;               /* sequences */
+    int32_t table_width;         /* pages a sequence can have */
+    int64_t table_stride;        /* elements between the table's rows, >= table_width */
+    const int32_t *page_table;   /* (device) [batch x table_width] */
+    const int32_t *seq_lens;     /* (device) [batch] */
+    const int32_t *cu_rows;      /* (device) [batch + 1], non-decreasing, starting at 0 */
+} llmint8_kv_cache;
+
+/*
+ * Quantize new tokens' keys and values into the cache. For every page and
+ * head that receives tokens, with old its absmax if the page already holds
+ * earlier tokens of the sequence and 0 if not:
+ *   S = max(old, max |new|); earlier codes become rint(code * (old / S)) if
+ *   S > old; new codes are rint(x * (127 / S)); the absmax becomes S
+ * in fp32, keys and values apart (S below 4e-37 gives codes 0). What a page
+ * held before its first token was written does not matter: pages need no
+ * clearing. A page that receives tokens belongs to one sequence; full pages
+ * may be shared.
+ *   K, V        (device) [tokens x heads x head_dim] of `type`; strides in
+ *               elements between tokens and between heads (multiples of 8,
+ *               not negative), so that they may be parts of a fused
+ *               projection's output. Values must be finite.
+ *   workspace   (device) >= 256 bytes, zeroed once (only its status word is used)
+ * Errors: LLMINT8_ERR_UNSUPPORTED_SHAPE for other page sizes or head
+ * dimensions, or pages * heads * page_size or table_width * page_size past
+ * 2^31; the others as everywhere. tokens == 0 or batch == 0 does nothing.
+ */
+LLMINT8_API llmint8_status llmint8_kv_append(const llmint8_kv_cache *cache, const void *K, const void *V, int type,
+                                 int64_t tokens, int64_t k_token_stride, int64_t k_head_stride,
+                                 int64_t v_token_stride, int64_t v_head_stride, void *workspace, size_t ws_bytes,
+                                 llmint8_stream_t stream);
+
+/* The reverse: the cached keys and values of each sequence's last positions
+ * as packed rows K, V (device) [tokens x heads x head_dim] of `type`, dense.
+ * Rows that belong to no sequence, or whose page is left out, are not
+ * written. Arguments and errors as llmint8_kv_append. */
+LLMINT8_API llmint8_status llmint8_kv_read(const llmint8_kv_cache *cache, void *K, void *V, int type, int64_t tokens,
+                               void *workspace, size_t ws_bytes, llmint8_stream_t stream);
+
+/* Bytes of workspace needed by llmint8_kv_attention. */
+LLMINT8_API size_t llmint8_kv_attention_workspace_size(int64_t heads, int64_t kv_heads, int64_t head_dim);
+
+/*
+ * Attention of packed new tokens over the cache (which holds their own keys
+ * and values already: llmint8_kv_append comes first). Query head g reads
+ * key/value head g / (heads / cache->heads). For row i of sequence b at
+ * position p_i, over the keys j <= p_i (causal) or all j < seq_lens[b]:
+ *   s_j = scale * q_i . k_j  [+ alibi_slopes[g] * (j - p_i)],
+ *   out_i = sum_j softmax(s)_j v_j,   lse_i = log sum_j exp(s_j)
+ * with k_j, v_j the cached values. Scores, softmax statistics and sums are
+ * held in fp32; the weights enter the value product as fp16. A row that no
+ * key is left for gives zeros and lse -inf.
+ *   Q            (device) [tokens x heads x head_dim] of `type`, strides as K
+ *   alibi_slopes (device, may be NULL) fp32 [heads]: the linear position
+ *                biases BLOOM adds to its scores
+ *   max_new      host-side upper bound of the new tokens of any one sequence,
+ *                0 if not known. It only chooses among kernels: with a wrong
+ *                value the result is the same.
+ *   out          (device) [tokens x heads x head_dim] of `type`, dense
+ *   lse          (device, may be NULL) fp32 [tokens x heads]
+ *   workspace    (device) >= llmint8_kv_attention_workspace_size bytes, zeroed once
+ * Errors: heads not a multiple of cache->heads is LLMINT8_ERR_UNSUPPORTED_SHAPE,
+ * a scale that is not finite LLMINT8_ERR_INVALID_ARG; the others as
+ * llmint8_kv_append. tokens == 0 or batch == 0 does nothing.
+ */
+LLMINT8_API llmint8_status llmint8_kv_attention(const llmint8_kv_cache *cache, const void *Q, int type,
+                                    int64_t tokens, int64_t heads, int64_t q_token_stride,
+                                    int64_t q_head_stride, float scale, int causal, const float *alibi_slopes,
+                                    int64_t max_new, void *out, float *lse, void *workspace, size_t ws_bytes,
+                                    llmint8_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -22,7 +22,8 @@ __all__ = [
     "matmul_mixed_fp16w",
     "workspace_size_fp16w", "ACTIVATIONS", "quantize_rowwise_asym", "code_row_sums", "workspace_size_asym",
     "matmul_mixed_asym", "MAX_K_ASYM", "quantize_rowwise_given", "matmul_codes", "bias_act_to_f16",
-    "gather_column_blocks", "OUT_F16", "OUT_F32", "outlier_bitmap",
+    "gather_column_blocks", "OUT_F16", "OUT_F32", "outlier_bitmap", "add_rmsnorm_quantize", "dequantize_rowwise",
+    "kv_append", "kv_read", "kv_attention_workspace_size", "kv_attention", "Int8KVCache",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libllmint8.so")
@@ -36,6 +37,14 @@ class _Debug(ctypes.Structure):
     _fields_ = [("codes", ctypes.c_void_p), ("row_absmax", ctypes.c_void_p), ("col_idx", ctypes.c_void_p),
                 ("count", ctypes.c_void_p), ("acc", ctypes.c_void_p), ("gemm_begin", ctypes.c_void_p),
                 ("gemm_end", ctypes.c_void_p)]
+
+
+class _KvCache(ctypes.Structure):
+    _fields_ = [("k_codes", ctypes.c_void_p), ("v_codes", ctypes.c_void_p), ("k_absmax", ctypes.c_void_p),
+                ("v_absmax", ctypes.c_void_p), ("pages", ctypes.c_int64), ("heads", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("batch", ctypes.c_int32),
+                ("table_width", ctypes.c_int32), ("table_stride", ctypes.c_int64), ("page_table", ctypes.c_void_p),
+                ("seq_lens", ctypes.c_void_p), ("cu_rows", ctypes.c_void_p)]
 
 
 _P = ctypes.c_void_p
@@ -71,6 +80,15 @@ _SIGNATURES = {
     "llmint8_workspace_size_asym": (ctypes.c_size_t, [_I64, _I64, _I64]),
     "llmint8_matmul_mixed_asym": (_ST, [_P, _I64, _I64, _P, _P, _P, _P, _I64, ctypes.c_float, _P, _P,
                                         ctypes.c_size_t, ctypes.POINTER(_Debug), _P]),
+    "llmint8_add_rmsnorm_quantize": (_ST, [_P, _P, _P, ctypes.c_int, _I64, _I64, ctypes.c_float, ctypes.c_float, _P,
+                                           _P, _P, _P, _P, _P, ctypes.c_size_t, _P]),
+    "llmint8_dequantize_rowwise": (_ST, [_P, _P, _I64, _I64, ctypes.c_int, _P, _P]),
+    "llmint8_kv_append": (_ST, [ctypes.POINTER(_KvCache), _P, _P, ctypes.c_int, _I64, _I64, _I64, _I64, _I64, _P,
+                                ctypes.c_size_t, _P]),
+    "llmint8_kv_read": (_ST, [ctypes.POINTER(_KvCache), _P, _P, ctypes.c_int, _I64, _P, ctypes.c_size_t, _P]),
+    "llmint8_kv_attention_workspace_size": (ctypes.c_size_t, [_I64, _I64, _I64]),
+    "llmint8_kv_attention": (_ST, [ctypes.POINTER(_KvCache), _P, ctypes.c_int, _I64, _I64, _I64, _I64, ctypes.c_float,
+                                   ctypes.c_int, _P, _I64, _P, _P, _P, ctypes.c_size_t, _P]),
 }
 EXPORTED = tuple(_SIGNATURES)
 NOALLOC_MAX_ROWS = NOALLOC_MAX_COLS = 65536
@@ -565,3 +583,248 @@ def gather_column_blocks(blocks, out=None):
     _check(load()["_gather_column_blocks"](blocks.data_ptr(), P, M, Nr, out.data_ptr(), _stream_ptr(blocks.device)),
            "llmint8_gather_column_blocks")
     return out
+
+
+# ---- around the linear in a transformer block: norm, key/value cache, attention ------
+
+TYPE_F16, TYPE_BF16 = 0, 1  # LLMINT8_TYPE_*
+
+
+def _value_type(t, name):
+    torch = _torch()
+    if t.dtype == torch.float16:
+        return TYPE_F16
+    if t.dtype == torch.bfloat16:
+        return TYPE_BF16
+    raise TypeError(f"{name} must be torch.float16 or torch.bfloat16, got {t.dtype}")
+
+
+def _need_like(t, name, dtype, shape, dev):
+    """A contiguous CUDA tensor of this type, shape and device."""
+    _need_cuda(t, name, dtype)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {list(shape)}, got {list(t.shape)}")
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, expected {dev}")
+
+
+def _call(where, dev, *args):
+    """An entry point on the current stream of `dev`, whichever device is current."""
+    torch = _torch()
+    if torch.cuda.current_device() == dev.index:
+        st = load()[where](*args, _stream_ptr(dev))
+    else:
+        with torch.cuda.device(dev):
+            st = load()[where](*args, _stream_ptr(dev))
+    _check(st, "llmint8" + where)
+
+
+def add_rmsnorm_quantize(X, weight, residual=None, eps: float = 1e-6, threshold: float = 0.0, codes=None,
+                         row_absmax=None, outlier_bitmap=None, Y=None, residual_out=None, workspace=None):
+    """(codes int8, row_absmax fp32, outlier_bitmap int32 words or None, Y fp16, residual_out) of
+    h = X + residual [rows x cols] (fp16 or bf16) and Y = h * weight / sqrt(mean(h^2) + eps):
+    the codes, row absmax and outlier columns are those of quantize_rowwise(Y, threshold)
+    (llmint8_add_rmsnorm_quantize). ``Y=False`` does not store Y (threshold <= 0 only; Y is
+    then returned as None). ``residual_out`` may be X or residual; without a residual it is
+    X unless given. With find_outlier_cols the results are matmul_codes' inputs."""
+    torch = _torch()
+    _need_cuda(X, "X")
+    kind = _value_type(X, "X")
+    if X.dim() != 2:
+        raise ValueError("X must be [rows x cols]")
+    rows, cols = X.shape
+    dev = X.device
+    _need_like(weight, "weight", X.dtype, (cols,), dev)
+    if residual is not None:
+        _need_like(residual, "residual", X.dtype, (rows, cols), dev)
+    if Y is False and 0 < threshold < float("inf"):
+        raise ValueError("Y is needed with a threshold: the linear takes its outlier columns from it")
+    if codes is None:
+        codes = torch.empty((rows, cols), dtype=torch.int8, device=dev)
+    else:
+        _need_like(codes, "codes", torch.int8, (rows, cols), dev)
+    if row_absmax is None:
+        row_absmax = torch.empty(rows, dtype=torch.float32, device=dev)
+    else:
+        _need_like(row_absmax, "row_absmax", torch.float32, (rows,), dev)
+    if outlier_bitmap is not None:
+        _need_like(outlier_bitmap, "outlier_bitmap", torch.int32, ((cols + 31) // 32,), dev)
+    elif threshold > 0:
+        outlier_bitmap = torch.empty((cols + 31) // 32, dtype=torch.int32, device=dev)
+    if Y is None:
+        Y = torch.empty((rows, cols), dtype=torch.float16, device=dev)
+    elif Y is False:
+        Y = None
+    else:
+        _need_like(Y, "Y", torch.float16, (rows, cols), dev)
+    if residual_out is not None:
+        _need_like(residual_out, "residual_out", X.dtype, (rows, cols), dev)
+    elif residual is not None:
+        residual_out = torch.empty_like(X)
+    ws = workspace if workspace is not None else get_workspace(quantize_workspace_size(rows, cols), dev)
+    _call("_add_rmsnorm_quantize", dev, X.data_ptr(), _ptr(residual), weight.data_ptr(), kind, rows, cols, float(eps),
+          float(threshold), _ptr(residual_out), _ptr(Y), codes.data_ptr(), row_absmax.data_ptr(),
+          _ptr(outlier_bitmap), ws.data_ptr(), ws.numel())
+    return codes, row_absmax, outlier_bitmap, Y, (X if residual_out is None else residual_out)
+
+
+def dequantize_rowwise(codes, row_absmax, dtype=None, out=None):
+    """codes int8 [rows x cols] times row_absmax / 127 as fp16 (or ``dtype``: torch.bfloat16)
+    (llmint8_dequantize_rowwise)."""
+    torch = _torch()
+    _need_cuda(codes, "codes", torch.int8)
+    if codes.dim() != 2:
+        raise ValueError("codes must be [rows x cols]")
+    rows, cols = codes.shape
+    dev = codes.device
+    _need_like(row_absmax, "row_absmax", torch.float32, (rows,), dev)
+    if out is None:
+        out = torch.empty((rows, cols), dtype=dtype or torch.float16, device=dev)
+    else:
+        _need_like(out, "out", dtype or out.dtype, (rows, cols), dev)
+    _call("_dequantize_rowwise", dev, codes.data_ptr(), row_absmax.data_ptr(), rows, cols, _value_type(out, "out"),
+          out.data_ptr())
+    return out
+
+
+def _kv_cache(k_codes, v_codes, k_absmax, v_absmax, page_table, seq_lens, cu_rows):
+    """The llmint8_kv_cache descriptor of checked tensors."""
+    torch = _torch()
+    _need_cuda(k_codes, "k_codes", torch.int8)
+    if k_codes.dim() != 4:
+        raise ValueError("k_codes must be [pages x heads x page_size x head_dim]")
+    pages, heads, page_size, head_dim = k_codes.shape
+    dev = k_codes.device
+    _need_like(v_codes, "v_codes", torch.int8, k_codes.shape, dev)
+    _need_like(k_absmax, "k_absmax", torch.float32, (pages, heads), dev)
+    _need_like(v_absmax, "v_absmax", torch.float32, (pages, heads), dev)
+    if page_table.dim() != 2 or page_table.dtype != torch.int32 or page_table.device != dev:
+        raise ValueError(f"page_table must be int32 [batch x pages of a sequence] on {dev}")
+    batch, width = page_table.shape
+    stride = page_table.stride(0) if batch > 1 else width
+    if (width > 1 and page_table.stride(1) != 1) or stride < width:
+        raise ValueError("page_table's rows must be contiguous and apart")
+    _need_like(seq_lens, "seq_lens", torch.int32, (batch,), dev)
+    _need_like(cu_rows, "cu_rows", torch.int32, (batch + 1,), dev)
+    return _KvCache(k_codes.data_ptr(), v_codes.data_ptr(), k_absmax.data_ptr(), v_absmax.data_ptr(), pages, heads,
+                    page_size, head_dim, batch, width, stride, page_table.data_ptr(), seq_lens.data_ptr(),
+                    cu_rows.data_ptr())
+
+
+def _need_rows(t, name, heads, head_dim, dev):
+    """Packed rows [tokens x heads x head_dim], fp16 or bf16, the last dimension dense."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor) or t.device != dev:
+        raise TypeError(f"{name} must be a tensor on {dev}")
+    kind = _value_type(t, name)
+    if t.dim() != 3 or t.shape[2] != head_dim or (heads is not None and t.shape[1] != heads):
+        raise ValueError(f"{name} must be [tokens x {heads or 'heads'} x {head_dim}], got {list(t.shape)}")
+    if t.stride(2) != 1:
+        raise ValueError(f"{name}'s last dimension must be contiguous")
+    return kind
+
+
+def _row_strides(t):
+    """Strides between tokens and between heads (0 where there is only one: it is never stepped)."""
+    tok, head, _ = t.stride()
+    return tok if t.shape[0] > 1 else 0, head if t.shape[1] > 1 else 0
+
+
+def kv_append(K, V, k_codes, v_codes, k_absmax, v_absmax, page_table, seq_lens, cu_rows, workspace=None):
+    """Quantize the new tokens' keys and values K, V [tokens x heads x head_dim] (fp16 or bf16,
+    strided views allowed) into the paged int8 cache k_codes, v_codes [pages x heads x page_size x
+    head_dim] with absmax k_absmax, v_absmax fp32 [pages x heads]. Rows cu_rows[b] .. cu_rows[b+1]
+    are the last positions of sequence b, whose length with them is seq_lens[b] and whose pages are
+    page_table[b] (llmint8_kv_append)."""
+    c = _kv_cache(k_codes, v_codes, k_absmax, v_absmax, page_table, seq_lens, cu_rows)
+    dev = k_codes.device
+    kind = _need_rows(K, "K", c.heads, c.head_dim, dev)
+    if _need_rows(V, "V", c.heads, c.head_dim, dev) != kind or V.shape != K.shape:
+        raise ValueError("K and V must have the same type and shape")
+    ws = workspace if workspace is not None else get_workspace(4096, dev)
+    _call("_kv_append", dev, ctypes.byref(c), K.data_ptr(), V.data_ptr(), kind, K.shape[0], *_row_strides(K),
+          *_row_strides(V), ws.data_ptr(), ws.numel())
+
+
+def kv_read(k_codes, v_codes, k_absmax, v_absmax, page_table, seq_lens, cu_rows, tokens: int, dtype=None, K=None,
+            V=None, workspace=None):
+    """(K, V) [tokens x heads x head_dim], fp16 (or ``dtype``): the cached values of each sequence's
+    last cu_rows[b+1] - cu_rows[b] positions as packed rows (llmint8_kv_read)."""
+    torch = _torch()
+    c = _kv_cache(k_codes, v_codes, k_absmax, v_absmax, page_table, seq_lens, cu_rows)
+    dev = k_codes.device
+    shape = (int(tokens), c.heads, c.head_dim)
+    dtype = dtype or (torch.float16 if K is None else K.dtype)
+    if K is None:
+        K = torch.empty(shape, dtype=dtype, device=dev)
+    else:
+        _need_like(K, "K", dtype, shape, dev)
+    if V is None:
+        V = torch.empty(shape, dtype=dtype, device=dev)
+    else:
+        _need_like(V, "V", dtype, shape, dev)
+    ws = workspace if workspace is not None else get_workspace(4096, dev)
+    _call("_kv_read", dev, ctypes.byref(c), K.data_ptr(), V.data_ptr(), _value_type(K, "K"), shape[0], ws.data_ptr(),
+          ws.numel())
+    return K, V
+
+
+def kv_attention_workspace_size(heads: int, kv_heads: int, head_dim: int) -> int:
+    return int(load()["_kv_attention_workspace_size"](heads, kv_heads, head_dim))
+
+
+def kv_attention(Q, k_codes, v_codes, k_absmax, v_absmax, page_table, seq_lens, cu_rows, scale: float | None = None,
+                 causal: bool = True, alibi_slopes=None, max_new: int = 0, out=None, lse=None, workspace=None):
+    """out [tokens x heads x head_dim] = attention of the packed new tokens Q (fp16 or bf16, strided
+    views allowed) over the paged int8 cache, which holds their own keys and values already
+    (kv_append comes first). ``scale`` defaults to head_dim ** -0.5; ``alibi_slopes`` fp32 [heads]
+    adds slope * (key position - query position) to the scores; ``lse`` fp32 [tokens x heads]
+    receives log sum exp; ``max_new``, an upper bound of the new tokens of one sequence (0:
+    unknown), only helps to choose the kernel (llmint8_kv_attention)."""
+    torch = _torch()
+    c = _kv_cache(k_codes, v_codes, k_absmax, v_absmax, page_table, seq_lens, cu_rows)
+    dev = k_codes.device
+    kind = _need_rows(Q, "Q", None, c.head_dim, dev)
+    tokens, heads = Q.shape[0], Q.shape[1]
+    if alibi_slopes is not None:
+        _need_like(alibi_slopes, "alibi_slopes", torch.float32, (heads,), dev)
+    if out is None:
+        out = torch.empty((tokens, heads, c.head_dim), dtype=Q.dtype, device=dev)
+    else:
+        _need_like(out, "out", Q.dtype, Q.shape, dev)
+    if lse is not None:
+        _need_like(lse, "lse", torch.float32, (tokens, heads), dev)
+    if scale is None:
+        scale = c.head_dim ** -0.5
+    if workspace is None:
+        workspace = get_workspace(kv_attention_workspace_size(heads, c.heads, c.head_dim), dev)
+    _call("_kv_attention", dev, ctypes.byref(c), Q.data_ptr(), kind, tokens, heads, *_row_strides(Q),
+          float(scale), int(bool(causal)), _ptr(alibi_slopes), int(max_new), out.data_ptr(), _ptr(lse),
+          workspace.data_ptr(), workspace.numel())
+    return out
+
+
+class Int8KVCache:
+    """The buffers of a paged int8 key/value cache, with the calls that work on them. Which pages
+    a sequence has (page_table), and its length, are the caller's to keep."""
+
+    def __init__(self, k_codes, v_codes, k_absmax, v_absmax):
+        self.k_codes, self.v_codes, self.k_absmax, self.v_absmax = k_codes, v_codes, k_absmax, v_absmax
+
+    @classmethod
+    def empty(cls, pages: int, heads: int, page_size: int, head_dim: int, device="cuda"):
+        torch = _torch()
+        codes = [torch.empty((pages, heads, page_size, head_dim), dtype=torch.int8, device=device) for _ in range(2)]
+        absmax = [torch.empty((pages, heads), dtype=torch.float32, device=device) for _ in range(2)]
+        return cls(*codes, *absmax)
+
+    def append(self, K, V, page_table, seq_lens, cu_rows):
+        kv_append(K, V, self.k_codes, self.v_codes, self.k_absmax, self.v_absmax, page_table, seq_lens, cu_rows)
+
+    def read(self, page_table, seq_lens, cu_rows, tokens: int, dtype=None):
+        return kv_read(self.k_codes, self.v_codes, self.k_absmax, self.v_absmax, page_table, seq_lens, cu_rows, tokens,
+                       dtype=dtype)
+
+    def attend(self, Q, page_table, seq_lens, cu_rows, **options):
+        return kv_attention(Q, self.k_codes, self.v_codes, self.k_absmax, self.v_absmax, page_table, seq_lens, cu_rows,
+                            **options)

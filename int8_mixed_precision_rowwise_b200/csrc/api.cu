@@ -65,6 +65,35 @@ llmint8_status check_k(int64_t K)
 
 llmint8_status cuda_status(cudaError_t e) { return e == cudaSuccess ? LLMINT8_OK : LLMINT8_ERR_CUDA; }
 
+bool value_type(int type) { return type == LLMINT8_TYPE_F16 || type == LLMINT8_TYPE_BF16; }
+
+// Strides of 16-bit rows in elements: every row starts on a 16-byte boundary.
+bool row_stride(int64_t s) { return s >= 0 && s % 8 == 0; }
+
+// The checks of a cache descriptor and its packed rows, for every entry point
+// that takes one. Only the workspace's status word is used here.
+llmint8_status check_cache(const llmint8_kv_cache *c, int64_t tokens, const void *workspace, size_t ws_bytes)
+{
+    if (!c || tokens < 0 || c->batch < 0 || c->pages < 0 || c->table_width < 0 || c->table_stride < c->table_width)
+        return LLMINT8_ERR_INVALID_ARG;
+    if ((c->head_dim != 64 && c->head_dim != 128) || c->heads <= 0 || c->heads > 65535 ||
+        (c->page_size != 16 && c->page_size != 32 && c->page_size != 64 && c->page_size != 128) ||
+        tokens > INT32_MAX || c->pages > INT32_MAX ||
+        c->pages * c->heads > (int64_t)INT32_MAX / c->page_size ||
+        (int64_t)c->table_width * c->page_size > INT32_MAX)
+        return LLMINT8_ERR_UNSUPPORTED_SHAPE;
+    const bool some = tokens > 0 && c->batch > 0; // without rows the arrays may be empty ones
+    if (!workspace || (some && (!c->k_codes || !c->v_codes || !c->k_absmax || !c->v_absmax || !c->page_table ||
+                                !c->seq_lens || !c->cu_rows)))
+        return LLMINT8_ERR_INVALID_ARG;
+    if (!aligned16(c->k_codes) || !aligned16(c->v_codes) || !aligned16(workspace) ||
+        (reinterpret_cast<uintptr_t>(c->k_absmax) & 3u) || (reinterpret_cast<uintptr_t>(c->v_absmax) & 3u) ||
+        (reinterpret_cast<uintptr_t>(c->page_table) & 3u) || (reinterpret_cast<uintptr_t>(c->seq_lens) & 3u) ||
+        (reinterpret_cast<uintptr_t>(c->cu_rows) & 3u))
+        return LLMINT8_ERR_ALIGNMENT;
+    return ws_bytes < (size_t)kHeaderBytes ? LLMINT8_ERR_WORKSPACE : LLMINT8_OK;
+}
+
 // The intermediate results a caller asked for in `dbg`: the raw int32
 // accumulators (with `run_acc`, one more int8 GEMM of the same codes; the
 // decode kernel writes them itself) and copies of the codes, row absmax and
@@ -445,6 +474,156 @@ llmint8_status llmint8_gemm_s8s8s32(const int8_t *A, int64_t M, const int8_t *B,
     g.Y = acc;
     g.status = ws.status;
     return cuda_status(launch_gemm(g, dev, stream));
+}
+
+llmint8_status llmint8_add_rmsnorm_quantize(const void *X, const void *residual, const void *weight, int type,
+                                            int64_t rows, int64_t cols, float eps, float threshold,
+                                            void *residual_out, void *Y_f16, int8_t *codes, float *row_absmax,
+                                            uint32_t *outlier_bitmap, void *workspace, size_t ws_bytes,
+                                            llmint8_stream_t stream)
+{
+    if (rows < 0 || !value_type(type) || !(eps >= 0.f) || std::isinf(eps))
+        return LLMINT8_ERR_INVALID_ARG;
+    llmint8_status st = check_k(cols);
+    if (st != LLMINT8_OK)
+        return st;
+    if (rows > INT32_MAX || rows * cols > (int64_t)1 << 40)
+        return LLMINT8_ERR_UNSUPPORTED_SHAPE;
+    const float t = effective_threshold(threshold);
+    if (!workspace || (t > 0.f && !outlier_bitmap) ||
+        (rows > 0 && (!X || !weight || !codes || !row_absmax || (t > 0.f && !Y_f16))))
+        return LLMINT8_ERR_INVALID_ARG;
+    if (!aligned16(X) || !aligned16(residual) || !aligned16(weight) || !aligned16(residual_out) ||
+        !aligned16(Y_f16) || !aligned16(codes) || !aligned16(row_absmax) || !aligned16(outlier_bitmap) ||
+        !aligned16(workspace))
+        return LLMINT8_ERR_ALIGNMENT;
+    Workspace ws;
+    const size_t need = carve(static_cast<char *>(workspace), rows, cols, false, false, &ws);
+    if (ws_bytes < need)
+        return LLMINT8_ERR_WORKSPACE;
+    if (outlier_bitmap && (rows == 0 || t <= 0.f)) { // no outlier columns: the bitmap is still written
+        if (cudaMemsetAsync(outlier_bitmap, 0, (size_t)((cols + 31) / 32) * 4, stream) != cudaSuccess)
+            return LLMINT8_ERR_CUDA;
+    }
+    if (rows == 0)
+        return LLMINT8_OK;
+    DeviceInfo dev;
+    if (device_info(&dev) != cudaSuccess)
+        return LLMINT8_ERR_CUDA;
+    const NormArgs a{X, residual, weight, type == LLMINT8_TYPE_BF16, rows, cols, eps, t, residual_out, Y_f16, codes,
+                     row_absmax, outlier_bitmap};
+    return cuda_status(launch_norm_quant(a, ws, dev, stream));
+}
+
+llmint8_status llmint8_dequantize_rowwise(const int8_t *codes, const float *row_absmax, int64_t rows, int64_t cols,
+                                          int type, void *out, llmint8_stream_t stream)
+{
+    if (rows < 0 || !value_type(type))
+        return LLMINT8_ERR_INVALID_ARG;
+    llmint8_status st = check_k(cols);
+    if (st != LLMINT8_OK)
+        return st;
+    if (rows > INT32_MAX || rows * cols > (int64_t)1 << 40)
+        return LLMINT8_ERR_UNSUPPORTED_SHAPE;
+    if (rows == 0)
+        return LLMINT8_OK;
+    if (!codes || !row_absmax || !out)
+        return LLMINT8_ERR_INVALID_ARG;
+    if (!aligned16(codes) || !aligned16(row_absmax) || !aligned16(out))
+        return LLMINT8_ERR_ALIGNMENT;
+    DeviceInfo dev;
+    if (device_info(&dev) != cudaSuccess)
+        return LLMINT8_ERR_CUDA;
+    return cuda_status(launch_dequant_rows(codes, row_absmax, rows, cols, out, type == LLMINT8_TYPE_BF16, dev, stream));
+}
+
+llmint8_status llmint8_kv_append(const llmint8_kv_cache *cache, const void *K, const void *V, int type,
+                                 int64_t tokens, int64_t k_token_stride, int64_t k_head_stride,
+                                 int64_t v_token_stride, int64_t v_head_stride, void *workspace, size_t ws_bytes,
+                                 llmint8_stream_t stream)
+{
+    llmint8_status st = check_cache(cache, tokens, workspace, ws_bytes);
+    if (st != LLMINT8_OK)
+        return st;
+    if (!value_type(type) || (tokens > 0 && (!K || !V)))
+        return LLMINT8_ERR_INVALID_ARG;
+    if (!aligned16(K) || !aligned16(V) || !row_stride(k_token_stride) || !row_stride(k_head_stride) ||
+        !row_stride(v_token_stride) || !row_stride(v_head_stride))
+        return LLMINT8_ERR_ALIGNMENT;
+    if (tokens == 0 || cache->batch == 0)
+        return LLMINT8_OK;
+    DeviceInfo dev;
+    if (device_info(&dev) != cudaSuccess)
+        return LLMINT8_ERR_CUDA;
+    const KvRows rows{K, V, k_token_stride, k_head_stride, v_token_stride, v_head_stride, tokens,
+                      type == LLMINT8_TYPE_BF16};
+    return cuda_status(launch_kv_append(*cache, rows, static_cast<uint32_t *>(workspace), dev, stream));
+}
+
+llmint8_status llmint8_kv_read(const llmint8_kv_cache *cache, void *K, void *V, int type, int64_t tokens,
+                               void *workspace, size_t ws_bytes, llmint8_stream_t stream)
+{
+    llmint8_status st = check_cache(cache, tokens, workspace, ws_bytes);
+    if (st != LLMINT8_OK)
+        return st;
+    if (!value_type(type) || (tokens > 0 && (!K || !V)))
+        return LLMINT8_ERR_INVALID_ARG;
+    if (!aligned16(K) || !aligned16(V))
+        return LLMINT8_ERR_ALIGNMENT;
+    if (tokens == 0 || cache->batch == 0)
+        return LLMINT8_OK;
+    DeviceInfo dev;
+    if (device_info(&dev) != cudaSuccess)
+        return LLMINT8_ERR_CUDA;
+    return cuda_status(launch_kv_read(*cache, K, V, tokens, type == LLMINT8_TYPE_BF16,
+                                      static_cast<uint32_t *>(workspace), dev, stream));
+}
+
+size_t llmint8_kv_attention_workspace_size(int64_t heads, int64_t kv_heads, int64_t head_dim)
+{
+    if (heads <= 0 || kv_heads <= 0 || head_dim <= 0)
+        return 0;
+    return carve(nullptr, 0, 0, false, false, nullptr);
+}
+
+llmint8_status llmint8_kv_attention(const llmint8_kv_cache *cache, const void *Q, int type, int64_t tokens,
+                                    int64_t heads, int64_t q_token_stride, int64_t q_head_stride, float scale,
+                                    int causal, const float *alibi_slopes, int64_t max_new, void *out, float *lse,
+                                    void *workspace, size_t ws_bytes, llmint8_stream_t stream)
+{
+    llmint8_status st = check_cache(cache, tokens, workspace, ws_bytes);
+    if (st != LLMINT8_OK)
+        return st;
+    if (!value_type(type) || (tokens > 0 && (!Q || !out)) || heads <= 0 || max_new < 0 || std::isnan(scale) || std::isinf(scale))
+        return LLMINT8_ERR_INVALID_ARG;
+    if (heads % cache->heads != 0 || heads > 65535)
+        return LLMINT8_ERR_UNSUPPORTED_SHAPE;
+    if (!aligned16(Q) || !aligned16(out) || !row_stride(q_token_stride) || !row_stride(q_head_stride) ||
+        (reinterpret_cast<uintptr_t>(alibi_slopes) & 3u) || (reinterpret_cast<uintptr_t>(lse) & 3u))
+        return LLMINT8_ERR_ALIGNMENT;
+    Workspace ws;
+    carve(static_cast<char *>(workspace), 0, 0, false, false, &ws);
+    if (ws_bytes < llmint8_kv_attention_workspace_size(heads, cache->heads, cache->head_dim))
+        return LLMINT8_ERR_WORKSPACE;
+    if (tokens == 0 || cache->batch == 0)
+        return LLMINT8_OK;
+    DeviceInfo dev;
+    if (device_info(&dev) != cudaSuccess)
+        return LLMINT8_ERR_CUDA;
+    AttnArgs a{};
+    a.q = Q;
+    a.q_token = q_token_stride;
+    a.q_head = q_head_stride;
+    a.tokens = tokens;
+    a.heads = (int)heads;
+    a.bf16 = type == LLMINT8_TYPE_BF16;
+    a.causal = causal != 0;
+    a.scale = scale;
+    a.slopes = alibi_slopes;
+    a.max_new = max_new > 0 ? max_new : tokens;
+    a.out = out;
+    a.lse = lse;
+    return cuda_status(launch_kv_attention(*cache, a, ws, dev, stream));
 }
 
 } // extern "C"

@@ -3,6 +3,7 @@
 #pragma once
 
 #include <cstdint>
+#include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
 #include "ptx.cuh"
@@ -42,6 +43,26 @@ __device__ __forceinline__ bool grid_barrier(uint32_t *sync, uint32_t nblocks, u
             return false;
         __nanosleep(32);
     }
+}
+
+// Two packed 16-bit values as fp32, and back (round to nearest even).
+template <bool BF16>
+__device__ __forceinline__ float2 up2(uint32_t v)
+{
+    if (BF16)
+        return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xFFFF0000u));
+    return __half22float2(*reinterpret_cast<const __half2 *>(&v));
+}
+
+template <bool BF16>
+__device__ __forceinline__ uint32_t down2(float a, float b)
+{
+    if (BF16) {
+        const __nv_bfloat162 r = __floats2bfloat162_rn(a, b);
+        return *reinterpret_cast<const uint32_t *>(&r);
+    }
+    const __half2 r = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&r);
 }
 
 // Per 16-byte vector (8 fp16 values): |x| as half2 pairs and their maximum.

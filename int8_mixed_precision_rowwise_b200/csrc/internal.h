@@ -38,6 +38,8 @@ inline int64_t gather_stride_m(int64_t M) { return (M + 3) / 4 * 4; }
 //   [24]     uint32 calls of the shared-memory quantizer so far
 //   [32]     uint64 arrivals at the shared-memory quantizer's grid barrier so
 //            far (one per CTA per call: a multiple of the grid between calls)
+//   [40]     uint32 CTAs of the norm's fix-up kernel that have finished (0
+//            between calls)
 //   [256]    uint32 two outlier bitmaps [2][kSetWords] of the shared-memory
 //            quantizer: call n ORs into set[n & 1] and clears set[(n+1) & 1]
 //            for the next call. Their place and size depend on no shape, so
@@ -70,6 +72,7 @@ struct Workspace {
     uint32_t *sets;   // [2][kSetWords]
     uint32_t *calls;
     unsigned long long *arrivals;
+    uint32_t *ticket;
     int32_t *col_idx;
     float *sx;
     int8_t *cx;
@@ -130,6 +133,7 @@ inline size_t carve(char *base, int64_t M, int64_t K, bool with_codes, bool deco
         ws->sets = reinterpret_cast<uint32_t *>(tg);
         ws->calls = hdr ? reinterpret_cast<uint32_t *>(hdr + 24) : nullptr;
         ws->arrivals = hdr ? reinterpret_cast<unsigned long long *>(hdr + 32) : nullptr;
+        ws->ticket = hdr ? reinterpret_cast<uint32_t *>(hdr + 40) : nullptr;
         ws->col_idx = reinterpret_cast<int32_t *>(ci);
         ws->sx = reinterpret_cast<float *>(sx);
         ws->cx = reinterpret_cast<int8_t *>(cx);
@@ -157,6 +161,25 @@ struct DeviceInfo {
 
 // Cached per-device properties (first call per device queries them).
 cudaError_t device_info(DeviceInfo *out);
+
+// Launch with programmatic stream serialization: the kernel may start while
+// the one before it in the stream still runs, and waits for it (griddep_wait)
+// before it touches global memory.
+template <typename... Args>
+cudaError_t launch_pdl(void (*kern)(Args...), dim3 grid, int block, size_t smem, cudaStream_t stream, Args... args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)block);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, args...);
+}
 
 // Quantize rows of X (fp16) with outlier detection at threshold t: codes,
 // absmax over the non-outlier columns, the outlier bitmap and (t > 0) its
@@ -260,6 +283,50 @@ struct DecodeArgs {
 
 bool decode_fused_fits(int64_t M, int64_t N, int64_t K, const DeviceInfo &dev);
 cudaError_t launch_decode(const DecodeArgs &args, const DeviceInfo &dev, cudaStream_t stream);
+
+// Residual addition, RMS norm and int8 quantization of [rows x cols] values
+// of one 16-bit type (llmint8_add_rmsnorm_quantize); null: not read or stored.
+struct NormArgs {
+    const void *x, *res, *w;
+    bool bf16;
+    int64_t rows, cols;
+    float eps, t;
+    void *h, *y;
+    int8_t *codes;
+    float *absmax;
+    uint32_t *bitmap;
+};
+cudaError_t launch_norm_quant(const NormArgs &args, const Workspace &ws, const DeviceInfo &dev, cudaStream_t stream);
+cudaError_t launch_dequant_rows(const int8_t *codes, const float *absmax, int64_t rows, int64_t cols, void *out,
+                                bool bf16, const DeviceInfo &dev, cudaStream_t stream);
+
+// The paged int8 key/value cache (llmint8_kv_cache) and 16-bit rows of
+// [token][head][head_dim] values with their strides in elements.
+struct KvRows {
+    const void *k, *v;
+    int64_t k_token, k_head, v_token, v_head;
+    int64_t tokens;
+    bool bf16;
+};
+cudaError_t launch_kv_append(const llmint8_kv_cache &c, const KvRows &rows, uint32_t *status, const DeviceInfo &dev,
+                             cudaStream_t stream);
+cudaError_t launch_kv_read(const llmint8_kv_cache &c, void *k, void *v, int64_t tokens, bool bf16, uint32_t *status,
+                           const DeviceInfo &dev, cudaStream_t stream);
+
+struct AttnArgs {
+    const void *q;
+    int64_t q_token, q_head; // strides in elements
+    int64_t tokens;
+    int heads;
+    bool bf16, causal;
+    float scale;
+    const float *slopes; // [heads] or null
+    int64_t max_new;     // at most so many new tokens a sequence, as far as the host knows
+    void *out;           // [tokens x heads x head_dim]
+    float *lse;          // [tokens x heads] or null
+};
+cudaError_t launch_kv_attention(const llmint8_kv_cache &c, const AttnArgs &a, const Workspace &ws,
+                                const DeviceInfo &dev, cudaStream_t stream);
 
 // Row-major int8 [rows x K] as a 2-D TMA tensor map (128-byte x box_rows box,
 // 128-byte swizzle, zero fill out of bounds); cached per device and buffer.
