@@ -519,8 +519,8 @@ typedef struct llmint8_kv_cache {
  *               projection's output. Values must be finite.
  *   workspace   (device) >= 256 bytes, zeroed once (only its status word is used)
  * Errors: LLMINT8_ERR_UNSUPPORTED_SHAPE for other page sizes or head
- * dimensions, or pages * heads * page_size or table_width * page_size past
- * 2^31; the others as everywhere. tokens == 0 or batch == 0 does nothing.
+ * dimensions, pages * heads * page_size past 2^31, or table_width * page_size
+ * past 2^30; the others as everywhere. tokens == 0 or batch == 0 does nothing.
  */
 LLMINT8_API llmint8_status llmint8_kv_append(const llmint8_kv_cache *cache, const void *K, const void *V, int type,
                                  int64_t tokens, int64_t k_token_stride, int64_t k_head_stride,

@@ -80,7 +80,7 @@ llmint8_status check_cache(const llmint8_kv_cache *c, int64_t tokens, const void
         (c->page_size != 16 && c->page_size != 32 && c->page_size != 64 && c->page_size != 128) ||
         tokens > INT32_MAX || c->pages > INT32_MAX ||
         c->pages * c->heads > (int64_t)INT32_MAX / c->page_size ||
-        (int64_t)c->table_width * c->page_size > INT32_MAX)
+        (int64_t)c->table_width * c->page_size > (int64_t)1 << 30)
         return LLMINT8_ERR_UNSUPPORTED_SHAPE;
     const bool some = tokens > 0 && c->batch > 0; // without rows the arrays may be empty ones
     if (!workspace || (some && (!c->k_codes || !c->v_codes || !c->k_absmax || !c->v_absmax || !c->page_table ||
@@ -583,7 +583,7 @@ size_t llmint8_kv_attention_workspace_size(int64_t heads, int64_t kv_heads, int6
 {
     if (heads <= 0 || kv_heads <= 0 || head_dim <= 0)
         return 0;
-    return carve(nullptr, 0, 0, false, false, nullptr);
+    return carve(nullptr, 0, 0, false, false, nullptr, 0, attn_slot_floats(head_dim));
 }
 
 llmint8_status llmint8_kv_attention(const llmint8_kv_cache *cache, const void *Q, int type, int64_t tokens,
@@ -602,8 +602,7 @@ llmint8_status llmint8_kv_attention(const llmint8_kv_cache *cache, const void *Q
         (reinterpret_cast<uintptr_t>(alibi_slopes) & 3u) || (reinterpret_cast<uintptr_t>(lse) & 3u))
         return LLMINT8_ERR_ALIGNMENT;
     Workspace ws;
-    carve(static_cast<char *>(workspace), 0, 0, false, false, &ws);
-    if (ws_bytes < llmint8_kv_attention_workspace_size(heads, cache->heads, cache->head_dim))
+    if (ws_bytes < carve(static_cast<char *>(workspace), 0, 0, false, false, &ws, 0, attn_slot_floats(cache->head_dim)))
         return LLMINT8_ERR_WORKSPACE;
     if (tokens == 0 || cache->batch == 0)
         return LLMINT8_OK;

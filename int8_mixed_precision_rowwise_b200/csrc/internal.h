@@ -16,6 +16,7 @@ namespace llmint8 {
 constexpr int kDecodeMaxM = 32;
 constexpr int kDecodeMaxCtas = 160;
 constexpr int kHeaderBytes = 256;
+constexpr int kAttnMaxCtas = 320; // CTAs of an attention kernel that split the work
 constexpr size_t kSetWords = (LLMINT8_MAX_K + 31) / 32; // bitmap words of the widest X
 // Outlier columns whose operands the prefill GEMM's epilogue reads from
 // per-call gathered copies (more columns: it gathers them in place).
@@ -45,6 +46,8 @@ inline int64_t gather_stride_m(int64_t M) { return (M + 3) / 4 * 4; }
 //            for the next call. Their place and size depend on no shape, so
 //            that whatever shapes share the workspace nothing else is
 //            written there.
+//   ...      uint32 arrivals at split items of the attention [kAttnMaxCtas], 0
+//            between calls (their place depends on no shape either)
 //   ...      uint32 outlier bitmap [ceil(K/32)]
 //   ...      int32  ascending outlier columns [K]
 //   ...      fp32   SX [M]
@@ -86,6 +89,8 @@ struct Workspace {
     int64_t np, mp;
     int32_t *sk_part; // null without the stream-K regions
     uint32_t *sk_flag;
+    uint32_t *attn_arrived;
+    float *attn_slots; // null but for attention
     size_t bytes;
 };
 
@@ -96,9 +101,10 @@ inline bool decode_shape(int64_t M, int64_t N) { return M >= 1 && M <= kDecodeMa
 
 // Lay out (base != null) or size a workspace; `decode` adds the regions of
 // the fused decode kernel, gather_n > 0 those of the prefill GEMM's gathered
-// outlier operands for an N-row weight.
+// outlier operands for an N-row weight, attn_slots the parked parts (floats) of
+// an attention's split items.
 inline size_t carve(char *base, int64_t M, int64_t K, bool with_codes, bool decode, Workspace *ws,
-                    int64_t gather_n = 0)
+                    int64_t gather_n = 0, size_t attn_slots = 0)
 {
     size_t off = 0;
     auto take = [&](size_t n) {
@@ -108,6 +114,7 @@ inline size_t carve(char *base, int64_t M, int64_t K, bool with_codes, bool deco
     };
     char *hdr = take(kHeaderBytes);
     char *tg = take(kSetWords * 8);
+    char *aa = take((size_t)kAttnMaxCtas * 4);
     size_t nwords = (size_t)((K + 31) / 32);
     char *bm = take(nwords * 4);
     char *ci = take((size_t)K * 4);
@@ -125,7 +132,10 @@ inline size_t carve(char *base, int64_t M, int64_t K, bool with_codes, bool deco
     const bool sk = gather_n > 0 && M >= 256;
     char *skp = sk ? take((size_t)kSkMaxPairs * kSkSlotBytes) : nullptr;
     char *skf = sk ? take((size_t)kSkMaxPairs * 2 * 4) : nullptr;
+    char *as = attn_slots ? take(attn_slots * 4) : nullptr;
     if (ws) {
+        ws->attn_arrived = reinterpret_cast<uint32_t *>(aa);
+        ws->attn_slots = reinterpret_cast<float *>(as);
         ws->status = reinterpret_cast<uint32_t *>(hdr);
         ws->count = hdr ? reinterpret_cast<int32_t *>(hdr + 4) : nullptr;
         ws->sync = hdr ? reinterpret_cast<uint32_t *>(hdr + 8) : nullptr;
@@ -308,6 +318,8 @@ struct KvRows {
     int64_t tokens;
     bool bf16;
 };
+struct KvView;
+KvView kv_view(const llmint8_kv_cache &c, uint32_t *status);
 cudaError_t launch_kv_append(const llmint8_kv_cache &c, const KvRows &rows, uint32_t *status, const DeviceInfo &dev,
                              cudaStream_t stream);
 cudaError_t launch_kv_read(const llmint8_kv_cache &c, void *k, void *v, int64_t tokens, bool bf16, uint32_t *status,
@@ -325,6 +337,9 @@ struct AttnArgs {
     void *out;           // [tokens x heads x head_dim]
     float *lse;          // [tokens x heads] or null
 };
+// Floats of the parked parts: two slots a CTA, each 16 rows of values and two
+// statistics.
+inline size_t attn_slot_floats(int64_t head_dim) { return (size_t)kAttnMaxCtas * 2 * 16 * (size_t)(head_dim + 2); }
 cudaError_t launch_kv_attention(const llmint8_kv_cache &c, const AttnArgs &a, const Workspace &ws,
                                 const DeviceInfo &dev, cudaStream_t stream);
 

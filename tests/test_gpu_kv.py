@@ -132,7 +132,7 @@ def test_pages_outside_the_cache_are_left_out(lib):
     bad = table.clone()
     bad[0, 1], bad[1, 0] = -1, pages
     narrow = bad[:, :3]  # sequence 0 needs four
-    ws = torch.zeros(1 << 16, dtype=torch.uint8, device="cuda")
+    ws = torch.zeros(lib.kv_attention_workspace_size(heads, heads, dim), dtype=torch.uint8, device="cuda")
     K, V = rows((100, heads, dim), g, F16), rows((100, heads, dim), g, F16)
     for t in (cache.k_codes, cache.v_codes):
         t.fill_(5)
