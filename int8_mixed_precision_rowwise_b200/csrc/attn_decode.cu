@@ -11,9 +11,9 @@
 // The value scale rides on the exponent, so that the weights that enter the
 // product are at most 1 (no overflow of fp16) and the codes stay exact.
 // q . kc and w . vc run on the tensor cores (fp16 in, fp32 sums). With row
-// tiles of 8 the other 8 rows of the m16 tile carry what rounding w to fp16
-// left over (w = hi + lo), which the matrix instruction then adds for free;
-// with 16 rows the weights are fp16 (off by at most 2^-11 of themselves).
+// tiles of 8 the weights enter as hi + lo, what rounding to fp16 left over in
+// a second product: there the matrix instructions have time to spare. With 16
+// rows the weights are fp16 (off by at most 2^-11 of themselves).
 //
 // Work. Unit: 128 keys of one (sequence, head, row tile). The units of all of
 // them in order are split evenly over the CTAs, whatever the lengths; a CTA
@@ -22,12 +22,19 @@
 // l) in the workspace, and the last to arrive adds the parts in order (so the
 // result does not depend on the order of arrival).
 //
-// Each of the four warps takes every fourth 32 keys of a segment and streams
-// them through a ring of its own: lane 0 issues the TMA loads of the pages two
-// or three steps ahead (page numbers and scales are fetched a step earlier
-// still, so that no lane waits for them), the codes land in swizzled shared
-// memory, and each lane's 16-byte reads of them are free of bank conflicts and
-// already hold what the lane's operand fragments need.
+// One warp loads: its lanes look up the pages and scales of a unit's 16-key
+// groups two units ahead (so that no lookup is waited for) and issue one TMA
+// load each into a ring of three units. Four warps compute, 32 keys each. The
+// products are taken transposed, keys (then dimensions) as the m16 side and
+// the row tile as n8, so that no part of an instruction is spent on padding
+// when 8 rows or fewer share a head. Shared memory is swizzled by the TMA, a
+// lane's 16-byte reads are free of bank conflicts and hold exactly the codes
+// of its operand fragments: the order of the dimensions within a product and
+// of the output rows is free, and chosen for that.
+//
+// The running maximum m moves only when a score exceeds it by more than 2^6
+// in weight (fp16 holds that as well): then no maximum is reduced over the
+// warp and nothing rescaled for most units.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -40,20 +47,21 @@
 namespace llmint8 {
 namespace {
 
-constexpr int kWarps = 4;
-constexpr int kThreads = kWarps * 32;
+constexpr int kWarps = 4;             // that compute
+constexpr int kThreads = (kWarps + 1) * 32;
 constexpr int kSub = 32;              // keys a warp takes at once
 constexpr int kUnit = kSub * kWarps;  // keys of a unit
+constexpr int kGroups = kUnit / 16;   // 16 keys lie in one page
 constexpr int kStages = 3;
-constexpr int kMergeRows = 8;
+constexpr float kSlack = 6.f;         // log2 of how far a weight may exceed 1
 
 template <int D>
 struct Smem {
-    static constexpr int kTile = kSub * D;                       // codes of one operand
-    static constexpr int kRing = kWarps * kStages * 2 * kTile;
-    static constexpr int kMerge = kWarps * kMergeRows * D * 4;
-    static constexpr int kMeta = kWarps * kStages * 2 * 2 * 4;   // (key scale, value scale) per 16 keys
-    static constexpr int kBars = kWarps * kStages * 8;
+    static constexpr int kTile = kUnit * D; // a unit's codes of one operand
+    static constexpr int kRing = kStages * 2 * kTile;
+    static constexpr int kMerge = kWarps * 8 * D * 4;
+    static constexpr int kMeta = kStages * kGroups * 16; // key scale, log2 value scale, 1 / value scale
+    static constexpr int kBars = kStages * 2 * 8;
     static constexpr int kStats = kWarps * 16 * 2 * 4;
     static constexpr int kTotal = kRing + kMerge + kMeta + kBars + kStats + 64;
 };
@@ -65,6 +73,20 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a
                  "{%0, %1, %2, %3};"
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// The 8 x 8 matrix of 16-bit values spread over the warp (lane 4 r + c holds
+// columns 2 c, 2 c + 1 of row r), transposed.
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t v)
+{
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
+}
+
+__device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes)
+{
+    asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
 }
 
 __device__ __forceinline__ uint4 lds128(uint32_t a)
@@ -151,35 +173,37 @@ struct Walk {
     }
 };
 
-template <int D, bool R8, bool ALIBI>
+template <int D, int NQ, bool ALIBI>
 __global__ void __launch_bounds__(kThreads, 2) k_attn_decode(const __grid_constant__ CUtensorMap km,
                                                              const __grid_constant__ CUtensorMap vm,
                                                              const AttnParams p)
 {
     using L = Smem<D>;
-    constexpr int TR = R8 ? 8 : 16;
-    constexpr int KS = D / 16;       // k-steps of q . k, and words a lane holds of a key
-    constexpr int NT = D / 8;        // n-tiles of w . v
+    constexpr int TR = 8 * NQ;  // rows of a tile
+    constexpr bool kLo = NQ == 1;
+    constexpr int KS = D / 16;  // k-steps of q . k, and words a lane holds of a key
+    constexpr int MT = D / 16;  // m-tiles of w . v
     constexpr uint32_t kTile = L::kTile;
     extern __shared__ __align__(1024) uint8_t smem[];
     const uint32_t ring = smem_u32(smem);
     float *s_merge = reinterpret_cast<float *>(smem + L::kRing);
-    float2 *s_meta = reinterpret_cast<float2 *>(smem + L::kRing + L::kMerge);
+    float *s_meta = reinterpret_cast<float *>(smem + L::kRing + L::kMerge);
     uint64_t *s_bars = reinterpret_cast<uint64_t *>(smem + L::kRing + L::kMerge + L::kMeta);
     float2 *s_ml = reinterpret_cast<float2 *>(smem + L::kRing + L::kMerge + L::kMeta + L::kBars); // [warp][16]
     int64_t *s_start = reinterpret_cast<int64_t *>(smem + L::kTotal - 64);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const KvView &c = p.c;
+    const uint32_t full = smem_u32(s_bars), empty = full + kStages * 8;
 
-    if (lane == 0) {
+    if (tid == 0) {
 #pragma unroll
-        for (int s = 0; s < kStages; ++s)
-            mbar_init(smem_u32(&s_bars[warp * kStages + s]), 1);
-        fence_barrier_init();
-        if (warp == 0) {
-            tma_prefetch_desc(&km);
-            tma_prefetch_desc(&vm);
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(full + s * 8, 1);
+            mbar_init(empty + s * 8, kWarps);
         }
+        fence_barrier_init();
+        tma_prefetch_desc(&km);
+        tma_prefetch_desc(&vm);
     }
     griddep_wait();
     griddep_release();
@@ -188,295 +212,331 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_decode(const __grid_consta
     const Range range = my_range<kThreads>(p, s_merge, s_start);
     if (range.u0 >= range.u1)
         return;
-
-    const int page_shift = c.page_shift;
-    const int box = page_shift >= 5 ? 32 : 16; // rows a TMA load brings
-    const uint32_t bar0 = smem_u32(&s_bars[warp * kStages]);
-    const uint32_t ring_w = ring + warp * (kStages * 2 * kTile);
-    float2 *meta_w = s_meta + warp * kStages * 2;
-
-    // ---- the loads: a cursor that runs ahead of the computation
-    Walk<TR> ahead;
-    Seg a;
-    ahead.start(p, range.u0, range.u1, range.b, range.off);
-    int at = 0;                 // next key of the cursor
-    bool more = ahead.next(a);  // the cursor has a segment
-    if (more)
-        at = a.t0 + warp * kSub;
-    auto settle = [&] { // on to a segment with keys for this warp
-        while (more && at >= a.t1) {
-            more = ahead.next(a);
-            if (more)
-                at = a.t0 + warp * kSub;
-        }
-    };
-    settle();
-    const int half = (lane & 1) * 16; // lanes look after the 16 keys of their parity
-    auto page_at = [&](int key) { // page of `key`, -1 if it has none
-        const int j = key >> page_shift;
-        int page = -1;
-        if (j < c.table_width)
-            page = __ldg(c.table + a.b * c.table_stride + j);
-        return page;
-    };
-    int page_next = more && at + half < a.t1 ? page_at(at + half) : -1;
-    float ka_pend = 0.f, va_pend = 0.f; // scales fetched for the last issue, stored at the next
-    int stage_pend = -1;
-    bool bad_pend = false;
-    int issued = 0;
-    uint32_t bad_any = 0;
-    auto store_meta = [&] {
-        if (stage_pend >= 0 && lane < 2) {
-            // An absent page weighs nothing: scale 0, weight 2^-inf.
-            const float ks = ka_pend * (1.0f / 127.0f) * p.scale_log2;
-            const float vs = bad_pend ? -1.f : fmaxf(va_pend * (1.0f / 127.0f), 1e-30f);
-            meta_w[stage_pend * 2 + lane] = make_float2(bad_pend ? 0.f : ks, vs);
-        }
-        stage_pend = -1;
-    };
-    auto issue = [&] {
-        store_meta();
-        if (!more)
-            return;
-        const int s = issued % kStages;
-        const bool want = at + half < a.t1;
-        const bool ok = want && (unsigned)page_next < (unsigned)c.pages;
-        if (want && !ok)
-            bad_any = 1;
-        const int block = page_next * c.heads + a.h; // fits: pages * heads * page_size < 2^31
-        ka_pend = ok ? __ldg(c.ka + block) : 0.f;
-        va_pend = ok ? __ldg(c.va + block) : 0.f;
-        bad_pend = !ok;
-        stage_pend = s;
-        const int y = (block << page_shift) + ((at + half) & (c.page_size - 1));
-        const uint32_t dst = ring_w + s * 2 * kTile, bar = bar0 + s * 8;
-        const bool ok1 = __shfl_sync(0xffffffffu, ok, 1);
-        if (box == 32) {
-            if (lane == 0) {
-                if (ok) {
-                    mbar_arrive_expect_tx(bar, 2 * kTile);
-                    tma_load_2d(dst, &km, bar, 0, y);
-                    tma_load_2d(dst + kTile, &vm, bar, 0, y);
-                } else {
-                    mbar_arrive(bar);
-                }
-            }
-        } else {
-            if (lane == 0)
-                mbar_arrive_expect_tx(bar, ((ok ? 1u : 0u) + (ok1 ? 1u : 0u)) * kTile);
-            __syncwarp();
-            if (lane < 2 && ok) {
-                tma_load_2d(dst + lane * (kTile / 2), &km, bar, 0, y);
-                tma_load_2d(dst + kTile + lane * (kTile / 2), &vm, bar, 0, y);
-            }
-        }
-        ++issued;
-        at += kUnit;
-        settle();
-        page_next = more && at + half < a.t1 ? page_at(at + half) : -1;
-    };
-#pragma unroll
-    for (int s = 0; s < kStages - 1; ++s)
-        issue();
-
-    // ---- the computation
     Walk<TR> walk;
     Seg q;
     walk.start(p, range.u0, range.u1, range.b, range.off);
+
+    if (warp == kWarps) {
+        // ------------------------------------------------ the loads
+        // Lane j looks after group j's keys, lane j + 8 after its values.
+        const int group = lane & 7, page_shift = c.page_shift;
+        const bool is_v = lane >= 8;
+        const int box = page_shift >= 5 ? 32 : 16; // rows a TMA load brings
+        const bool loads = lane < 16 && (group * 16) % box == 0;
+        bool more = walk.next(q);
+        int at = more ? q.t0 : 0;
+        struct Unit {
+            bool some;  // there is a unit
+            int page;   // of this lane's group, -1 if none or not wanted
+            bool want;
+            int h, slot;
+            float scale;
+        };
+        // The unit after the last one, its page number requested.
+        auto fetch = [&](Unit &u) {
+            while (more && at >= q.t1) {
+                more = walk.next(q);
+                if (more)
+                    at = q.t0;
+            }
+            u.some = more;
+            u.page = -1;
+            u.want = false;
+            if (!more)
+                return;
+            const int key = at + group * 16;
+            u.want = lane < 16 && key < q.t1;
+            const int j = key >> page_shift;
+            if (u.want && j < c.table_width)
+                u.page = __ldg(c.table + q.b * c.table_stride + j);
+            u.h = q.h;
+            u.slot = key & (c.page_size - 1);
+            at += kUnit;
+        };
+        bool bad = false, failed = false;
+        // Its scale requested, once the page number is there.
+        auto scale = [&](Unit &u) {
+            if (u.want && (unsigned)u.page >= (unsigned)c.pages) {
+                bad = true;
+                u.page = -1;
+            }
+            u.scale = u.page >= 0 ? __ldg((is_v ? c.va : c.ka) + (u.page * c.heads + u.h)) : 0.f;
+        };
+        Unit u0, u1, u2;
+        fetch(u0);
+        fetch(u1);
+        scale(u0);
+        for (int i = 0; u0.some; ++i) {
+            fetch(u2);
+            scale(u1);
+            const int s = i % kStages;
+            if (i >= kStages && !mbar_wait(empty + s * 8, ((i / kStages) - 1) & 1))
+                failed = true;
+            const bool load = loads && u0.page >= 0;
+            const uint32_t n = __popc(__ballot_sync(0xffffffffu, load));
+            failed = __any_sync(0xffffffffu, failed);
+            if (failed)
+                break;
+            const uint32_t bar = full + s * 8;
+            if (lane == 0)
+                mbar_expect_tx(bar, n * box * D);
+            __syncwarp();
+            if (load)
+                tma_load_2d(ring + (s * 2 + (is_v ? 1 : 0)) * kTile + group * 16 * D, is_v ? &vm : &km, bar, 0,
+                            ((u0.page * c.heads + u0.h) << page_shift) + u0.slot);
+            // A group without a page weighs nothing: scale 0, weight 2^-inf.
+            float *meta = s_meta + (s * kGroups + group) * 4;
+            if (lane < 8) {
+                meta[0] = u0.scale * (1.0f / 127.0f) * p.scale_log2;
+            } else if (lane < 16) {
+                const float vs = fmaxf(u0.scale * (1.0f / 127.0f), 1e-30f);
+                meta[1] = u0.page >= 0 ? log2f(vs) : -INFINITY;
+                meta[2] = u0.page >= 0 ? 1.0f / vs : 0.f;
+            }
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(bar);
+            u0 = u1;
+            u1 = u2;
+        }
+        if (bad)
+            atomicOr(c.status, LLMINT8_DEV_BAD_PAGE);
+        if (failed && lane == 0)
+            atomicOr(c.status, LLMINT8_DEV_TIMEOUT_PRODUCER);
+        return;
+    }
+
+    // ---------------------------------------------------- the computation
+    const int g = lane >> 2, t = lane & 3;
     int used = 0;
     bool failed = false;
     while (walk.next(q)) {
-        // Rows of this lane: g, and g + 8 with 16-row tiles.
-        uint32_t qa[KS][R8 ? 2 : 4];
-        float fac[R8 ? 1 : 2], slope[R8 ? 1 : 2];
-        int limit[R8 ? 1 : 2], pos[R8 ? 1 : 2]; // last key a row sees
+        // As an operand this lane holds dimensions t D/4 .. of row g (of each
+        // 8); of the scores it has rows 2 t and 2 t + 1.
+        uint32_t qb[NQ][KS][2];
+        float fac[NQ][2], slope[NQ][2];
+        int limit[NQ][2], pos[NQ][2]; // last key a row sees
+        const int64_t first_row = __ldg(c.cu + q.b);
 #pragma unroll
-        for (int i = 0; i < (R8 ? 1 : 2); ++i) {
+        for (int i = 0; i < NQ; ++i) {
             const int row = g + 8 * i;
             const bool live = row < q.rows;
             const int R = q.row0 + (live ? row : 0);
             const int tok = R / p.group, head = q.h * p.group + (R - tok * p.group);
-            pos[i] = q.len - q.n + tok;
-            limit[i] = !live ? INT32_MAX // nobody reads its result
-                       : pos[i] < 0 ? -1 : p.causal ? min(pos[i], q.keys - 1) : q.keys - 1;
-            slope[i] = ALIBI ? __ldg(p.slopes + head) * 1.44269504f : 0.f;
-            const uint4 *src = reinterpret_cast<const uint4 *>(
-                static_cast<const uint16_t *>(p.q) + (__ldg(c.cu + q.b) + (int64_t)tok) * p.q_token + head * p.q_head +
-                t * (D / 4));
+            const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.q) +
+                                                               (first_row + tok) * p.q_token + head * p.q_head +
+                                                               t * (D / 4));
             uint32_t w[2 * KS];
 #pragma unroll
             for (int v = 0; v < KS / 2; ++v)
                 reinterpret_cast<uint4 *>(w)[v] = live ? __ldg(src + v) : make_uint4(0, 0, 0, 0);
-            fac[i] = 1.f;
+            float f = 1.f;
             if (p.bf16)
-                fac[i] = bf16_row_to_f16<2 * KS>(w);
+                f = bf16_row_to_f16<2 * KS>(w);
 #pragma unroll
             for (int k = 0; k < KS; ++k) {
-                qa[k][i] = w[2 * k];
-                qa[k][(R8 ? 1 : 2) + i] = w[2 * k + 1];
+                qb[i][k][0] = w[2 * k];
+                qb[i][k][1] = w[2 * k + 1];
+            }
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int r2 = 2 * t + e;
+                fac[i][e] = __shfl_sync(0xffffffffu, f, 4 * r2);
+                const bool live2 = r2 + 8 * i < q.rows;
+                const int R2 = q.row0 + (live2 ? r2 + 8 * i : 0);
+                const int tok2 = R2 / p.group;
+                pos[i][e] = q.len - q.n + tok2;
+                limit[i][e] = !live2 ? INT32_MAX // nobody reads its result
+                              : pos[i][e] < 0 ? -1 : p.causal ? min(pos[i][e], q.keys - 1) : q.keys - 1;
+                slope[i][e] = ALIBI ? __ldg(p.slopes + q.h * p.group + (R2 - tok2 * p.group)) * 1.44269504f : 0.f;
             }
         }
-        const int lim_min = warp_min(R8 ? limit[0] : min(limit[0], limit[1]));
-        float o[NT][4];
+        int lim_min = INT32_MAX;
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+        for (int i = 0; i < NQ; ++i)
+            lim_min = min(lim_min, min(limit[i][0], limit[i][1]));
+        lim_min = warp_min(lim_min);
+        float o[NQ][MT][4];
+        float m[NQ][2], l[NQ][2];
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                o[n][e] = 0.f;
-        float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-
-        for (int key = q.t0 + warp * kSub; key < q.t1; key += kUnit) {
-            issue();
-            const int s = used % kStages;
-            failed |= !mbar_wait(bar0 + s * 8, (used / kStages) & 1);
-            ++used;
-            __syncwarp();
-            const uint32_t kb = ring_w + s * 2 * kTile, vb = kb + kTile;
-            const float2 m0 = meta_w[s * 2], m1 = meta_w[s * 2 + 1];
-            float sc[4][4];
+        for (int i = 0; i < NQ; ++i) {
+            m[i][0] = m[i][1] = -INFINITY;
+            l[i][0] = l[i][1] = 0.f;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
+            for (int n = 0; n < MT; ++n)
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    sc[j][e] = 0.f;
-                const int row = 8 * j + g;
-                uint32_t w[KS];
-                if (D == 128) {
-                    *reinterpret_cast<uint4 *>(w) = lds128(kb + row * 128 + (((2 * t) ^ g) << 4));
-                    *reinterpret_cast<uint4 *>(w + 4) = lds128(kb + row * 128 + (((2 * t + 1) ^ g) << 4));
-                } else {
-                    *reinterpret_cast<uint4 *>(w) = lds128(kb + row * 64 + ((t ^ ((g >> 1) & 3)) << 4));
-                }
+                    o[i][n][e] = 0.f;
+        }
+
+        for (int unit = q.t0; unit < q.t1; unit += kUnit, ++used) {
+            const int s = used % kStages;
+            if (!failed) // one wait that runs out is enough
+                failed = !mbar_wait(full + s * 8, (used / kStages) & 1);
+            __syncwarp();
+            const int key = unit + warp * kSub;
+            if (key < q.t1) {
+                const uint32_t kb = ring + s * 2 * kTile + warp * kSub * D, vb = kb + kTile;
+                const float4 m0 = *reinterpret_cast<const float4 *>(s_meta + (s * kGroups + 2 * warp) * 4);
+                const float4 m1 = *reinterpret_cast<const float4 *>(s_meta + (s * kGroups + 2 * warp + 1) * 4);
+                // ---- scores: two m-tiles of 16 keys
+                float sc[NQ][2][4];
 #pragma unroll
-                for (int k = 0; k < KS; ++k) {
-                    uint32_t b0, b1;
-                    codes_to_f16(w[k], b0, b1);
-                    mma_16816(sc[j], qa[k][0], R8 ? 0u : qa[k][1], R8 ? qa[k][1] : qa[k][2], R8 ? 0u : qa[k][3], b0, b1);
-                }
-            }
-            // ---- scores to weights
-            const float lv0 = m0.y < 0.f ? -INFINITY : __log2f(m0.y), lv1 = m1.y < 0.f ? -INFINITY : __log2f(m1.y);
-            const float iv0 = m0.y < 0.f ? 0.f : __frcp_rn(m0.y), iv1 = m1.y < 0.f ? 0.f : __frcp_rn(m1.y);
-            const bool edge = key + kSub - 1 > lim_min;
-            uint32_t pa[4][R8 ? 2 : 2]; // [n-tile][row g: hi / row g + 8 (or lo)]
-            float alpha[2];
+                for (int a = 0; a < 2; ++a) {
+                    uint32_t w0[KS], w1[KS]; // codes of keys 16 a + g and 8 further
+                    if (D == 128) {
+                        const uint32_t ra = kb + (16 * a + g) * 128, x0 = ((2 * t) ^ g) << 4, x1 = x0 ^ 16;
+                        *reinterpret_cast<uint4 *>(w0) = lds128(ra + x0);
+                        *reinterpret_cast<uint4 *>(w0 + 4) = lds128(ra + x1);
+                        *reinterpret_cast<uint4 *>(w1) = lds128(ra + 1024 + x0);
+                        *reinterpret_cast<uint4 *>(w1 + 4) = lds128(ra + 1024 + x1);
+                    } else {
+                        const uint32_t ra = kb + (16 * a + g) * 64 + ((t ^ ((g >> 1) & 3)) << 4);
+                        *reinterpret_cast<uint4 *>(w0) = lds128(ra);
+                        *reinterpret_cast<uint4 *>(w1) = lds128(ra + 512);
+                    }
 #pragma unroll
-            for (int i = 0; i < (R8 ? 1 : 2); ++i) {
-                float top = -INFINITY;
+                    for (int i = 0; i < NQ; ++i)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float ks = (j < 2 ? m0.x : m1.x) * fac[i], lv = j < 2 ? lv0 : lv1;
+                        for (int e = 0; e < 4; ++e)
+                            sc[i][a][e] = 0.f;
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const int kk = key + 8 * j + 2 * t + e;
-                        float x = sc[j][2 * i + e] * ks;
-                        if (ALIBI)
-                            x = fmaf(slope[i], (float)(kk - pos[i]), x);
-                        x += lv;
-                        if (edge && kk > limit[i])
-                            x = -INFINITY;
-                        sc[j][2 * i + e] = x;
-                        top = fmaxf(top, x);
+                    for (int k = 0; k < KS; ++k) {
+                        uint32_t a0, a1, a2, a3;
+                        codes_to_f16(w0[k], a0, a2);
+                        codes_to_f16(w1[k], a1, a3);
+#pragma unroll
+                        for (int i = 0; i < NQ; ++i)
+                            mma_16816(sc[i][a], a0, a1, a2, a3, qb[i][k][0], qb[i][k][1]);
                     }
                 }
-                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                const float mn = fmaxf(m[i], top);
-                const float mu = mn == -INFINITY ? 0.f : mn;
-                alpha[i] = exp2_approx(m[i] - mu);
-                m[i] = mn;
-                float sum[2] = {0.f, 0.f};
+                // ---- to weights. sc[.][a][e]: key 16 a + g + 8 (e / 2), row 2 t + e % 2
+                const bool edge = key + kSub - 1 > lim_min;
+                uint32_t hi[NQ][2][2], lo[NQ][2][2];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float w0 = exp2_approx(sc[j][2 * i] - mu), w1 = exp2_approx(sc[j][2 * i + 1] - mu);
-                    sum[j >> 1] += w0 + w1;
-                    const uint32_t hi = down2<false>(w0, w1);
-                    pa[j][i] = hi;
-                    if (R8) {
-                        const float2 h = up2<false>(hi);
-                        pa[j][1] = down2<false>(w0 - h.x, w1 - h.y);
+                for (int i = 0; i < NQ; ++i) {
+                    bool over = false;
+#pragma unroll
+                    for (int a = 0; a < 2; ++a)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int kk = key + 16 * a + g + 8 * (e >> 1);
+                            float x = sc[i][a][e];
+                            if (ALIBI) {
+                                x = fmaf(x, (a ? m1.x : m0.x) * fac[i][e & 1], a ? m1.y : m0.y);
+                                x = fmaf(slope[i][e & 1], (float)(kk - pos[i][e & 1]), x);
+                            } else {
+                                x = fmaf(x, (a ? m1.x : m0.x) * fac[i][e & 1], a ? m1.y : m0.y);
+                            }
+                            if (edge && kk > limit[i][e & 1])
+                                x = -INFINITY;
+                            sc[i][a][e] = x;
+                            over |= x > m[i][e & 1] + kSlack;
+                        }
+                    if (__any_sync(0xffffffffu, over)) {
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            float top = fmaxf(fmaxf(sc[i][0][e], sc[i][0][2 + e]), fmaxf(sc[i][1][e], sc[i][1][2 + e]));
+                            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+                            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+                            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+                            const float mn = fmaxf(m[i][e], top);
+                            const float alpha = mn == -INFINITY ? 1.f : exp2_approx(m[i][e] - mn);
+                            m[i][e] = mn;
+                            l[i][e] *= alpha;
+#pragma unroll
+                            for (int n = 0; n < MT; ++n) {
+                                o[i][n][e] *= alpha;
+                                o[i][n][2 + e] *= alpha;
+                            }
+                        }
+                    }
+                    const float mu[2] = {m[i][0] == -INFINITY ? 0.f : m[i][0], m[i][1] == -INFINITY ? 0.f : m[i][1]};
+#pragma unroll
+                    for (int a = 0; a < 2; ++a) {
+                        const float iv = a ? m1.z : m0.z;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            sc[i][a][e] = exp2_approx(sc[i][a][e] - mu[e & 1]);
+                        l[i][0] = fmaf(sc[i][a][0] + sc[i][a][2], iv, l[i][0]);
+                        l[i][1] = fmaf(sc[i][a][1] + sc[i][a][3], iv, l[i][1]);
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const uint32_t h = down2<false>(sc[i][a][2 * e], sc[i][a][2 * e + 1]);
+                            if (kLo) {
+                                const float2 f = up2<false>(h);
+                                lo[i][a][e] = transpose8x8(
+                                    down2<false>(sc[i][a][2 * e] - f.x, sc[i][a][2 * e + 1] - f.y));
+                            }
+                            hi[i][a][e] = transpose8x8(h);
+                        }
                     }
                 }
-                l[i] = fmaf(l[i], alpha[i], fmaf(sum[0], iv0, sum[1] * iv1));
-            }
-            if (R8)
-                alpha[1] = alpha[0];
-            if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
+                // ---- weights times values: m-tile n holds this lane's dimensions
+                // 2 n (rows g) and 2 n + 1 (rows g + 8) of D / 8
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    o[n][0] *= alpha[0];
-                    o[n][1] *= alpha[0];
-                    o[n][2] *= alpha[1];
-                    o[n][3] *= alpha[1];
+                for (int a = 0; a < 2; ++a) {
+                    const int r0 = 16 * a + 2 * t;
+                    uint32_t v0[MT / 2], v1[MT / 2], v2[MT / 2], v3[MT / 2];
+                    if (D == 128) {
+                        const uint32_t ra = vb + r0 * 128, x0 = (g ^ (r0 & 7)) << 4, x1 = x0 ^ 16;
+                        *reinterpret_cast<uint4 *>(v0) = lds128(ra + x0);
+                        *reinterpret_cast<uint4 *>(v1) = lds128(ra + 128 + x1);
+                        *reinterpret_cast<uint4 *>(v2) = lds128(ra + 1024 + x0);
+                        *reinterpret_cast<uint4 *>(v3) = lds128(ra + 1152 + x1);
+                    } else {
+                        const uint32_t ra = vb + r0 * 64 + (((g >> 1) ^ ((r0 >> 1) & 3)) << 4) + (g & 1) * 8;
+                        *reinterpret_cast<uint2 *>(v0) = lds64(ra);
+                        *reinterpret_cast<uint2 *>(v1) = lds64(ra + 64);
+                        *reinterpret_cast<uint2 *>(v2) = lds64(ra + 512);
+                        *reinterpret_cast<uint2 *>(v3) = lds64(ra + 576);
+                    }
+#pragma unroll
+                    for (int w = 0; w < MT / 2; ++w) {
+                        uint32_t e0[4], e1[4];
+                        code_pairs_to_f16(v0[w], v1[w], e0);
+                        code_pairs_to_f16(v2[w], v3[w], e1);
+#pragma unroll
+                        for (int i = 0; i < NQ; ++i) {
+                            mma_16816(o[i][2 * w], e0[0], e0[1], e1[0], e1[1], hi[i][a][0], hi[i][a][1]);
+                            mma_16816(o[i][2 * w + 1], e0[2], e0[3], e1[2], e1[3], hi[i][a][0], hi[i][a][1]);
+                            if (kLo) {
+                                mma_16816(o[i][2 * w], e0[0], e0[1], e1[0], e1[1], lo[i][a][0], lo[i][a][1]);
+                                mma_16816(o[i][2 * w + 1], e0[2], e0[3], e1[2], e1[3], lo[i][a][0], lo[i][a][1]);
+                            }
+                        }
+                    }
                 }
             }
-            // ---- weights times values
-#pragma unroll
-            for (int ks = 0; ks < 2; ++ks) {
-                const int r0 = 16 * ks + 2 * t;
-                uint32_t v0[NT / 4], v1[NT / 4], v2[NT / 4], v3[NT / 4];
-                if (D == 128) {
-                    const uint32_t ra = vb + r0 * 128, x0 = (g ^ (r0 & 7)) << 4, x1 = (g ^ ((r0 + 1) & 7)) << 4;
-                    *reinterpret_cast<uint4 *>(v0) = lds128(ra + x0);
-                    *reinterpret_cast<uint4 *>(v1) = lds128(ra + 128 + x1);
-                    *reinterpret_cast<uint4 *>(v2) = lds128(ra + 1024 + x0);
-                    *reinterpret_cast<uint4 *>(v3) = lds128(ra + 1152 + x1);
-                } else {
-                    const uint32_t ra = vb + r0 * 64 + (((g >> 1) ^ ((r0 >> 1) & 3)) << 4) + (g & 1) * 8;
-                    *reinterpret_cast<uint2 *>(v0) = lds64(ra);
-                    *reinterpret_cast<uint2 *>(v1) = lds64(ra + 64);
-                    *reinterpret_cast<uint2 *>(v2) = lds64(ra + 512);
-                    *reinterpret_cast<uint2 *>(v3) = lds64(ra + 576);
-                }
-                const uint32_t a0 = pa[2 * ks][0], a1 = pa[2 * ks][1], a2 = pa[2 * ks + 1][0], a3 = pa[2 * ks + 1][1];
-#pragma unroll
-                for (int w = 0; w < NT / 4; ++w) {
-                    uint32_t b0[4], b1[4];
-                    code_pairs_to_f16(v0[w], v1[w], b0);
-                    code_pairs_to_f16(v2[w], v3[w], b1);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        mma_16816(o[4 * w + e], a0, a1, a2, a3, b0[e], b1[e]);
-                }
-            }
-            __syncwarp(); // the stage is read: the next issue may overwrite it
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(empty + s * 8);
         }
 
         // ---- the four warps' parts into one, 8 rows at a time
-#pragma unroll
-        for (int i = 0; i < (R8 ? 1 : 2); ++i) {
-            l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
-            l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
-            if (t == 0)
-                s_ml[warp * 16 + g + 8 * i] = make_float2(m[i], l[i]);
-        }
         const bool whole = q.c0 == 0 && q.c1 == q.chunks;
-        const int64_t out_row = (int64_t)__ldg(c.cu + q.b) * p.heads;
+        const int64_t out_row = first_row * p.heads;
         float *slot = p.slots + ((int64_t)blockIdx.x * 2 + (q.c0 == 0 ? 1 : 0)) * (16 * (D + 2));
 #pragma unroll
-        for (int i = 0; i < (R8 ? 1 : 2); ++i) {
-            if (i)
-                __syncthreads();
-            // This lane's dimensions of row g: the 2 NT from t D/4 on (n-tile
-            // n holds dimension n of each of its two columns' blocks).
-            float *dst = s_merge + (warp * kMergeRows + g) * D;
+        for (int i = 0; i < NQ; ++i) {
 #pragma unroll
-            for (int n = 0; n < NT; n += 4)
+            for (int e = 0; e < 2; ++e) {
+                float sum = l[i][e];
+                sum += __shfl_xor_sync(0xffffffffu, sum, 4);
+                sum += __shfl_xor_sync(0xffffffffu, sum, 8);
+                sum += __shfl_xor_sync(0xffffffffu, sum, 16);
+                const int row = 2 * t + e;
+                if (g == 0)
+                    s_ml[warp * 16 + row + 8 * i] = make_float2(m[i][e], sum);
+                // 16-byte chunks swizzled by row: rows are a multiple of all banks apart
+                float4 *dst = reinterpret_cast<float4 *>(s_merge + (warp * 8 + row) * D);
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    float4 v;
-                    if (R8)
-                        v = make_float4(o[n][e] + o[n][2 + e], o[n + 1][e] + o[n + 1][2 + e],
-                                        o[n + 2][e] + o[n + 2][2 + e], o[n + 3][e] + o[n + 3][2 + e]);
-                    else
-                        v = make_float4(o[n][2 * i + e], o[n + 1][2 * i + e], o[n + 2][2 * i + e],
-                                        o[n + 3][2 * i + e]);
-                    // 16-byte chunks swizzled by row: rows are a multiple of all banks apart
-                    const int chunk = ((2 * t + e) * NT + n) / 4;
-                    reinterpret_cast<float4 *>(dst)[chunk ^ g] = v;
-                }
-            __syncthreads();
-            for (int x = tid; x < kMergeRows * D / 4; x += kThreads) {
+                for (int n = 0; n < MT; n += 2)
+                    dst[(g * (D / 32) + n / 2) ^ t] =
+                        make_float4(o[i][n][e], o[i][n][2 + e], o[i][n + 1][e], o[i][n + 1][2 + e]);
+            }
+            named_barrier_sync(1, kWarps * 32);
+            for (int x = tid; x < 8 * D / 4; x += kWarps * 32) {
                 const int rr = x / (D / 4), ch = x % (D / 4), row = rr + 8 * i;
                 if (row >= q.rows)
                     break;
@@ -493,8 +553,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_decode(const __grid_consta
 #pragma unroll
                 for (int w = 0; w < kWarps; ++w) {
                     const float f = exp2_approx(ml[w].x - mu);
-                    const float4 v =
-                        reinterpret_cast<const float4 *>(s_merge + (w * kMergeRows + rr) * D)[ch ^ rr];
+                    const float4 v = reinterpret_cast<const float4 *>(s_merge + (w * 8 + rr) * D)[ch ^ (rr >> 1)];
                     lsum = fmaf(ml[w].y, f, lsum);
                     acc.x = fmaf(v.x, f, acc.x);
                     acc.y = fmaf(v.y, f, acc.y);
@@ -509,6 +568,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_decode(const __grid_consta
                         reinterpret_cast<float2 *>(slot + 16 * D)[row] = make_float2(M, lsum);
                 }
             }
+            named_barrier_sync(1, kWarps * 32); // the buffer is free
         }
         if (!whole) {
             // Parts lie in CTA `first` (its opening slot) and all CTAs to
@@ -517,18 +577,18 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_decode(const __grid_consta
             const int first = (int)(((begin + 1) * G - 1) / range.total);
             const int last = (int)(((begin + q.chunks) * G - 1) / range.total);
             __threadfence();
-            __syncthreads();
+            named_barrier_sync(1, kWarps * 32);
             if (tid == 0) {
                 const uint32_t old = atomicAdd(p.arrived + first, 1u);
                 const bool all = old == (uint32_t)(last - first);
                 if (all)
                     p.arrived[first] = 0u;
-                *reinterpret_cast<int *>(s_start) = all ? 1 : 0;
+                *reinterpret_cast<volatile int *>(s_start) = all ? 1 : 0;
             }
-            __syncthreads();
+            named_barrier_sync(1, kWarps * 32);
             if (*reinterpret_cast<volatile int *>(s_start)) {
                 __threadfence();
-                for (int x = tid; x < q.rows * (D / 4); x += kThreads) {
+                for (int x = tid; x < q.rows * (D / 4); x += kWarps * 32) {
                     const int row = x / (D / 4), ch = x % (D / 4);
                     float M = -INFINITY, lsum = 0.f;
                     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -548,20 +608,18 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_decode(const __grid_consta
                     finish_row<D>(p, out_row, q.h, q.row0 + row, ch, acc, M, lsum);
                 }
             }
+            named_barrier_sync(1, kWarps * 32);
         }
-        __syncthreads(); // the merge buffers are free
     }
-    if (bad_any)
-        atomicOr(c.status, LLMINT8_DEV_BAD_PAGE);
     if (failed && lane == 0)
-        atomicOr(c.status, LLMINT8_DEV_TIMEOUT_PRODUCER);
+        atomicOr(c.status, LLMINT8_DEV_TIMEOUT_EPILOGUE);
 }
 
-template <int D, bool R8>
+template <int D, int NQ>
 cudaError_t launch(const AttnParams &p, const CUtensorMap &km, const CUtensorMap &vm, int grid, int device,
                    cudaStream_t stream)
 {
-    auto kern = p.slopes ? k_attn_decode<D, R8, true> : k_attn_decode<D, R8, false>;
+    auto kern = p.slopes ? k_attn_decode<D, NQ, true> : k_attn_decode<D, NQ, false>;
     static std::atomic<uint64_t> configured[2];
     const uint64_t bit = 1ull << (device & 63);
     if (!(configured[p.slopes ? 1 : 0].load() & bit)) {
@@ -588,10 +646,10 @@ cudaError_t launch_attn_decode(AttnParams p, const llmint8_kv_cache &c, bool r8,
     p.unit = kUnit;
     const int grid = std::min(kAttnMaxCtas, 2 * dev.num_sms);
     if (c.head_dim == 128)
-        return r8 ? launch<128, true>(p, km, vm, grid, dev.device, stream)
-                  : launch<128, false>(p, km, vm, grid, dev.device, stream);
-    return r8 ? launch<64, true>(p, km, vm, grid, dev.device, stream)
-              : launch<64, false>(p, km, vm, grid, dev.device, stream);
+        return r8 ? launch<128, 1>(p, km, vm, grid, dev.device, stream)
+                  : launch<128, 2>(p, km, vm, grid, dev.device, stream);
+    return r8 ? launch<64, 1>(p, km, vm, grid, dev.device, stream)
+              : launch<64, 2>(p, km, vm, grid, dev.device, stream);
 }
 
 } // namespace llmint8
