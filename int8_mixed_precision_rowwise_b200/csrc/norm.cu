@@ -13,6 +13,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 
@@ -107,27 +108,121 @@ struct NormParams {
     int cols;
     float eps;
     __half t16;
-    uint32_t *sets, *calls, *ticket, *bitmap_out;
-    int alone; // one row: its own outlier columns are all there are
+    uint32_t *sets, *calls, *sync, *bitmap_out, *status;
 };
 
-// One CTA per row, the row in registers from its one read to its codes. With
-// THR a row is coded against the outlier columns it has itself; what other
-// rows add to the set is put right by k_norm_fix.
-template <bool BF16, bool THR>
-__global__ void __launch_bounds__(kMaxRowThreads) k_norm_quant(const NormParams p)
+constexpr int kListed = 1024; // outlier columns that the fix-up visits one by one
+
+// After every CTA has added its rows' outlier columns to the set: the complete
+// set into shared memory, the first kListed of its columns listed; CTA 0 also
+// writes it out, clears the other set for the next call and moves the call
+// counter on (everyone read it before the barrier). Returns the set's size,
+// or -1 if the barrier ran out.
+__device__ __forceinline__ int complete_set(const NormParams &p, uint32_t call, uint32_t *s_set, int *s_col)
 {
-    __shared__ float s_red[2][32];
+    __shared__ int s_count;
+    const int nwords = (p.cols + 31) >> 5, tid = threadIdx.x;
+    __threadfence();
+    __syncthreads();
+    if (tid == 0)
+        s_count = grid_barrier(p.sync, gridDim.x) ? 0 : -1 - 133143;
+    __syncthreads();
+    const uint32_t *set = p.sets + (call & 1u) * kSetWords;
+    for (int w = tid; w < nwords; w += blockDim.x) {
+        uint32_t v = __ldcg(set + w);
+        s_set[w] = v;
+        if (blockIdx.x == 0)
+            p.bitmap_out[w] = v;
+        while (v) {
+            const int b = __ffs(v) - 1;
+            v &= v - 1u;
+            const int at = atomicAdd(&s_count, 1);
+            if (at >= 0 && at < kListed)
+                s_col[at] = w * 32 + b;
+        }
+    }
+    if (blockIdx.x == 0) {
+        uint32_t *next = p.sets + ((call + 1u) & 1u) * kSetWords;
+        for (int w = tid; w < (int)kSetWords; w += blockDim.x)
+            next[w] = 0u;
+        if (tid == 0)
+            *reinterpret_cast<volatile uint32_t *>(p.calls) = call + 1u;
+    }
+    __syncthreads();
+    const int count = s_count;
+    if (count < 0 && tid == 0)
+        atomicOr(p.status, LLMINT8_DEV_TIMEOUT_QUANT);
+    return count;
+}
+
+// One warp puts a row right that was coded before the set was complete: its
+// codes in the set's columns become 0, and if its absmax was attained in one
+// of them it is coded again. All other codes stand: a row's absmax and codes
+// depend on the set only through those columns.
+__device__ __forceinline__ void fix_row(const NormParams &p, int64_t r, int count, const uint32_t *s_set,
+                                        const int *s_col)
+{
+    const int lane = threadIdx.x & 31, nvec = p.cols >> 3;
+    const __half *Y = reinterpret_cast<const __half *>(p.y) + r * p.cols;
+    int8_t *codes = reinterpret_cast<int8_t *>(p.codes) + r * p.cols;
+    const float old = p.absmax[r], t = __half2float(p.t16);
+    bool stale = count > kListed;
+    if (!stale)
+        for (int i = lane; i < count; i += 32) {
+            const int c = s_col[i];
+            const float a = fabsf(__half2float(Y[c]));
+            if (a < t && codes[c] != 0) {
+                codes[c] = 0;
+                stale |= a == old;
+            }
+        }
+    if (!__any_sync(0xffffffffu, stale))
+        return;
+    const uint4 *yr = p.y + r * nvec;
+    __half2 m2 = __float2half2_rn(0.f);
+    for (int c = lane; c < nvec; c += 32) {
+        uint4 v = yr[c];
+        mask_known(v, (s_set[c >> 2] >> ((c & 3) * 8)) & 0xFFu);
+        __half2 a[4];
+        m2 = __hmax2(m2, vec_abs_max(v, a));
+    }
+    const float amax = warp_all<true>(fmaxf(__low2float(m2), __high2float(m2)));
+    const float s = amax > 0.f ? __fdiv_rn(127.0f, amax) : 0.f;
+    for (int c = lane; c < nvec; c += 32) {
+        uint4 v = yr[c];
+        mask_known(v, (s_set[c >> 2] >> ((c & 3) * 8)) & 0xFFu);
+        p.codes[r * nvec + c] = codes8(v, s);
+    }
+    if (lane == 0)
+        p.absmax[r] = amax;
+}
+
+// One CTA per row, the row in registers from its one read to its codes. With
+// THR a row is coded against the outlier columns known by then (its own and
+// what earlier rows of any CTA have found); after all rows a grid barrier
+// makes the set complete. The CTA's last row is still in registers and is
+// coded again from there where the set has grown; with many rows the columns
+// are known after the first few, so the others rarely need fix_row's work.
+template <bool BF16, bool THR, int MAXT>
+__global__ void __launch_bounds__(MAXT, 1024 / MAXT) k_norm_quant(const NormParams p)
+{
+    __shared__ float s_red[3][32];
+    extern __shared__ uint32_t s_dyn[]; // THR: the set, then its listed columns
     const int tid = threadIdx.x, nwarps = blockDim.x >> 5;
     const int nvec = p.cols >> 3;
     griddep_wait();
     griddep_release();
-    uint32_t *set = nullptr;
-    if (THR)
-        set = p.sets + (*reinterpret_cast<volatile uint32_t *>(p.calls) & 1u) * kSetWords;
-    for (int64_t r = blockIdx.x; r < p.rows; r += gridDim.x) {
+    uint32_t call = 0u, *set = nullptr;
+    if (THR) {
+        call = *reinterpret_cast<volatile uint32_t *>(p.calls);
+        set = p.sets + (call & 1u) * kSetWords;
+    }
+    uint4 v[kVec];
+    float amax = 0.f;
+    int64_t r = blockIdx.x;
+    for (; r < p.rows; r += gridDim.x) {
         const uint4 *xr = p.x + r * nvec;
-        uint4 v[kVec];
+        uint32_t known[kVec];
 #pragma unroll
         for (int i = 0; i < kVec; ++i) {
             const int c = tid + i * blockDim.x;
@@ -145,6 +240,13 @@ __global__ void __launch_bounds__(kMaxRowThreads) k_norm_quant(const NormParams 
             for (int i = 0; i < kVec; ++i)
                 v[i] = add8<BF16>(v[i], u[i]);
         }
+        if (THR) {
+#pragma unroll
+            for (int i = 0; i < kVec; ++i) {
+                const int c = tid + i * blockDim.x;
+                known[i] = c < nvec ? (__ldcg(set + (c >> 2)) >> ((c & 3) * 8)) & 0xFFu : 0u;
+            }
+        }
         float ss = 0.f;
 #pragma unroll
         for (int i = 0; i < kVec; ++i) {
@@ -155,7 +257,6 @@ __global__ void __launch_bounds__(kMaxRowThreads) k_norm_quant(const NormParams 
         }
         ss = block_all<false>(ss, s_red[0], nwarps);
         const float rstd = 1.0f / sqrtf(ss / (float)p.cols + p.eps);
-        float amax = 0.f;
         __half2 m2 = __float2half2_rn(0.f);
 #pragma unroll
         for (int i = 0; i < kVec; ++i) {
@@ -166,13 +267,17 @@ __global__ void __launch_bounds__(kMaxRowThreads) k_norm_quant(const NormParams 
                     p.y[r * nvec + c] = v[i];
                 __half2 a[4];
                 __half2 m = vec_abs_max(v[i], a);
-                if (THR && __hge(__hmax(__low2half(m), __high2half(m)), p.t16)) {
-                    const uint32_t hit = hit_mask8(v[i], p.t16);
-                    const uint32_t bits = hit << ((c & 3) * 8);
-                    if ((__ldcg(set + (c >> 2)) & bits) != bits)
-                        atomicOr(set + (c >> 2), bits);
-                    mask_known(v[i], hit);
-                    m = vec_abs_max(v[i], a);
+                if (THR) {
+                    if (__hge(__hmax(__low2half(m), __high2half(m)), p.t16)) {
+                        const uint32_t hit = hit_mask8(v[i], p.t16);
+                        if (hit & ~known[i])
+                            atomicOr(set + (c >> 2), hit << ((c & 3) * 8));
+                        known[i] |= hit;
+                    }
+                    if (known[i]) {
+                        mask_known(v[i], known[i]);
+                        m = vec_abs_max(v[i], a);
+                    }
                 }
                 m2 = __hmax2(m2, m);
             }
@@ -188,21 +293,60 @@ __global__ void __launch_bounds__(kMaxRowThreads) k_norm_quant(const NormParams 
         if (tid == 0)
             p.absmax[r] = amax;
     }
+    if (THR) {
+        uint32_t *s_set = s_dyn;
+        int *s_col = reinterpret_cast<int *>(s_dyn + ((p.cols + 31) >> 5));
+        const int count = complete_set(p, call, s_set, s_col);
+        if (count <= 0)
+            return;
+        // The last row, from registers.
+        bool more = false;
+        __half2 m2 = __float2half2_rn(0.f);
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) {
+            const int c = tid + i * blockDim.x;
+            if (c < nvec) {
+                const uint4 was = v[i];
+                mask_known(v[i], (s_set[c >> 2] >> ((c & 3) * 8)) & 0xFFu);
+                more |= was.x != v[i].x || was.y != v[i].y || was.z != v[i].z || was.w != v[i].w;
+                __half2 a[4];
+                m2 = __hmax2(m2, vec_abs_max(v[i], a));
+            }
+        }
+        r -= gridDim.x; // this CTA's last row
+        if (__syncthreads_or(more)) {
+            amax = block_all<true>(fmaxf(__low2float(m2), __high2float(m2)), s_red[2], nwarps);
+            const float s = amax > 0.f ? __fdiv_rn(127.0f, amax) : 0.f;
+#pragma unroll
+            for (int i = 0; i < kVec; ++i) {
+                const int c = tid + i * blockDim.x;
+                if (c < nvec)
+                    p.codes[r * nvec + c] = codes8(v[i], s);
+            }
+            if (tid == 0)
+                p.absmax[r] = amax;
+        }
+        for (int64_t k = blockIdx.x + (int64_t)(tid >> 5) * gridDim.x; k < r; k += (int64_t)nwarps * gridDim.x)
+            fix_row(p, k, count, s_set, s_col);
+    }
 }
 
 // Rows wider than the registers hold: the same steps, each pass reading h (or
 // x) again.
 template <bool BF16, bool THR>
-__global__ void __launch_bounds__(kMaxRowThreads) k_norm_quant_wide(const NormParams p)
+__global__ void __launch_bounds__(kMaxRowThreads, 1) k_norm_quant_wide(const NormParams p)
 {
     __shared__ float s_red[2][32];
+    extern __shared__ uint32_t s_dyn[];
     const int tid = threadIdx.x, nwarps = blockDim.x >> 5;
     const int nvec = p.cols >> 3;
     griddep_wait();
     griddep_release();
-    uint32_t *set = nullptr;
-    if (THR)
-        set = p.sets + (*reinterpret_cast<volatile uint32_t *>(p.calls) & 1u) * kSetWords;
+    uint32_t call = 0u, *set = nullptr;
+    if (THR) {
+        call = *reinterpret_cast<volatile uint32_t *>(p.calls);
+        set = p.sets + (call & 1u) * kSetWords;
+    }
     for (int64_t r = blockIdx.x; r < p.rows; r += gridDim.x) {
         float ss = 0.f;
         auto hidden = [&](int c) {
@@ -246,89 +390,14 @@ __global__ void __launch_bounds__(kMaxRowThreads) k_norm_quant_wide(const NormPa
         if (tid == 0)
             p.absmax[r] = amax;
     }
-}
-
-// After every row has added its outlier columns to the set: the columns of
-// the set get code 0 in every row, and a row whose absmax is attained in one
-// of them is coded again. All other codes stand: a row's absmax and codes
-// depend on the set only through those columns. The last CTA to finish moves
-// the call counter on, so that the next call finds the other set, cleared
-// here, and the counter untouched until everyone has read it.
-__global__ void __launch_bounds__(256) k_norm_fix(const NormParams p)
-{
-    extern __shared__ uint32_t s_dyn[];
-    const int nwords = (p.cols + 31) >> 5, nvec = p.cols >> 3;
-    uint32_t *s_set = s_dyn;
-    int *s_col = reinterpret_cast<int *>(s_dyn + nwords); // the first kListed columns
-    constexpr int kListed = 1024;
-    __shared__ int s_count;
-    const int tid = threadIdx.x, lane = tid & 31;
-    griddep_wait();
-    griddep_release();
-    const uint32_t call = *reinterpret_cast<volatile uint32_t *>(p.calls);
-    const uint32_t *set = p.sets + (call & 1u) * kSetWords;
-    uint32_t *next = p.sets + ((call + 1u) & 1u) * kSetWords;
-    if (tid == 0)
-        s_count = 0;
-    __syncthreads();
-    for (int w = tid; w < nwords; w += blockDim.x) {
-        uint32_t v = __ldcg(set + w);
-        s_set[w] = v;
-        if (blockIdx.x == 0)
-            p.bitmap_out[w] = v;
-        while (v) {
-            const int b = __ffs(v) - 1;
-            v &= v - 1u;
-            const int at = atomicAdd(&s_count, 1);
-            if (at < kListed)
-                s_col[at] = w * 32 + b;
-        }
-    }
-    if (blockIdx.x == 0)
-        for (int w = tid; w < (int)kSetWords; w += blockDim.x)
-            next[w] = 0u;
-    __syncthreads();
-    const int count = s_count;
-    const __half *Y = reinterpret_cast<const __half *>(p.y);
-    if (count) {
-        const int64_t nw = (int64_t)gridDim.x * (blockDim.x >> 5);
-        for (int64_t r = (int64_t)blockIdx.x * (blockDim.x >> 5) + (tid >> 5); r < p.rows; r += nw) {
-            const float old = __ldcg(p.absmax + r);
-            bool stale = count > kListed;
-            if (!stale)
-                for (int i = lane; i < count; i += 32) {
-                    const int c = s_col[i];
-                    const float a = fabsf(__half2float(Y[r * (int64_t)p.cols + c]));
-                    if (a < __half2float(p.t16)) {
-                        reinterpret_cast<int8_t *>(p.codes)[r * (int64_t)p.cols + c] = 0;
-                        stale |= a == old;
-                    }
-                }
-            if (!__any_sync(0xffffffffu, stale))
-                continue;
-            const uint4 *yr = p.y + r * nvec;
-            __half2 m2 = __float2half2_rn(0.f);
-            for (int c = lane; c < nvec; c += 32) {
-                uint4 v = yr[c];
-                mask_known(v, (s_set[c >> 2] >> ((c & 3) * 8)) & 0xFFu);
-                __half2 a[4];
-                m2 = __hmax2(m2, vec_abs_max(v, a));
-            }
-            const float amax = warp_all<true>(fmaxf(__low2float(m2), __high2float(m2)));
-            const float s = amax > 0.f ? __fdiv_rn(127.0f, amax) : 0.f;
-            for (int c = lane; c < nvec; c += 32) {
-                uint4 v = yr[c];
-                mask_known(v, (s_set[c >> 2] >> ((c & 3) * 8)) & 0xFFu);
-                p.codes[r * nvec + c] = codes8(v, s);
-            }
-            if (lane == 0)
-                p.absmax[r] = amax;
-        }
-    }
-    __syncthreads();
-    if (tid == 0 && atomicAdd(p.ticket, 1u) == gridDim.x - 1u) {
-        *p.ticket = 0u;
-        *reinterpret_cast<volatile uint32_t *>(p.calls) = call + 1u;
+    if (THR) {
+        uint32_t *s_set = s_dyn;
+        int *s_col = reinterpret_cast<int *>(s_dyn + ((p.cols + 31) >> 5));
+        const int count = complete_set(p, call, s_set, s_col);
+        if (count > 0)
+            for (int64_t k = blockIdx.x + (int64_t)(tid >> 5) * gridDim.x; k < p.rows;
+                 k += (int64_t)nwarps * gridDim.x)
+                fix_row(p, k, count, s_set, s_col);
     }
 }
 
@@ -372,22 +441,49 @@ cudaError_t launch_norm_quant(const NormArgs &a, const Workspace &ws, const Devi
     p.t16 = threshold_fp16(a.t);
     p.sets = ws.sets;
     p.calls = ws.calls;
-    p.ticket = ws.ticket;
+    p.sync = ws.sync;
     p.bitmap_out = a.bitmap;
+    p.status = ws.status;
     const int nvec = p.cols >> 3;
     const int threads = std::min(kMaxRowThreads, (nvec + 32 * kVec - 1) / (32 * kVec) * 32);
-    const bool wide = nvec > kMaxRowThreads * kVec;
-    auto kern = wide ? (a.bf16 ? (thr ? k_norm_quant_wide<true, true> : k_norm_quant_wide<true, false>)
-                               : (thr ? k_norm_quant_wide<false, true> : k_norm_quant_wide<false, false>))
-                     : (a.bf16 ? (thr ? k_norm_quant<true, true> : k_norm_quant<true, false>)
-                               : (thr ? k_norm_quant<false, true> : k_norm_quant<false, false>));
-    const int64_t grid = std::min<int64_t>(a.rows, (int64_t)dev.num_sms * std::max(1, 2048 / threads));
-    cudaError_t e = launch_pdl(kern, dim3((unsigned)grid), threads, 0, stream, p);
-    if (e != cudaSuccess || !thr)
-        return e;
-    const size_t smem = ((size_t)(p.cols + 31) / 32 + 1024) * 4;
-    const int64_t fgrid = std::min<int64_t>((a.rows + 7) / 8, (int64_t)dev.num_sms * 8);
-    return launch_pdl(k_norm_fix, dim3((unsigned)fgrid), 256, smem, stream, p);
+    const int size = nvec > kMaxRowThreads * kVec ? 2 : threads > 512 ? 1 : 0; // wide rows; large CTAs
+    using Kernel = void (*)(NormParams);
+    static const Kernel kernels[3][2][2] = {
+        {{k_norm_quant<false, false, 512>, k_norm_quant<false, true, 512>},
+         {k_norm_quant<true, false, 512>, k_norm_quant<true, true, 512>}},
+        {{k_norm_quant<false, false, kMaxRowThreads>, k_norm_quant<false, true, kMaxRowThreads>},
+         {k_norm_quant<true, false, kMaxRowThreads>, k_norm_quant<true, true, kMaxRowThreads>}},
+        {{k_norm_quant_wide<false, false>, k_norm_quant_wide<false, true>},
+         {k_norm_quant_wide<true, false>, k_norm_quant_wide<true, true>}}};
+    const Kernel kern = kernels[size][a.bf16][thr];
+    const size_t smem = thr ? ((size_t)(p.cols + 31) / 32 + kListed) * 4 : 0;
+    // The grid barrier needs every CTA resident: as many as fit, asked once
+    // per variant and CTA size (at the largest shared memory the variant uses).
+    static std::atomic<int> resident[64][3][2][2][kMaxRowThreads / 32 + 1];
+    std::atomic<int> &fit = resident[dev.device & 63][size][a.bf16][thr][threads / 32];
+    int per_sm = fit.load();
+    if (per_sm == 0) {
+        const size_t most = thr ? (std::min<size_t>(kSetWords, size == 2 ? kSetWords : kMaxRowThreads * kVec / 4) + kListed) * 4 : 0;
+        cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, threads, most);
+        if (e != cudaSuccess)
+            return e;
+        if (per_sm < 1)
+            return cudaErrorLaunchOutOfResources;
+        fit.store(per_sm);
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)std::min<int64_t>(a.rows, (int64_t)dev.num_sms * per_sm));
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeCooperative;
+    attr[1].val.cooperative = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = thr ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
 cudaError_t launch_dequant_rows(const int8_t *codes, const float *absmax, int64_t rows, int64_t cols, void *out,
