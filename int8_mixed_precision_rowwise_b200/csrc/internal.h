@@ -39,6 +39,8 @@ inline int64_t gather_stride_m(int64_t M) { return (M + 3) / 4 * 4; }
 //   [24]     uint32 calls of the shared-memory quantizer so far
 //   [32]     uint64 arrivals at the shared-memory quantizer's grid barrier so
 //            far (one per CTA per call: a multiple of the grid between calls)
+//   [40]     uint32 growth of the norm's outlier sets so far (compared with an
+//            earlier value only; never cleared after workspace_init)
 //   [256]    uint32 two outlier bitmaps [2][kSetWords] of the shared-memory
 //            quantizer: call n ORs into set[n & 1] and clears set[(n+1) & 1]
 //            for the next call. Their place and size depend on no shape, so
@@ -73,6 +75,7 @@ struct Workspace {
     uint32_t *sets;   // [2][kSetWords]
     uint32_t *calls;
     unsigned long long *arrivals;
+    uint32_t *grown;
     int32_t *col_idx;
     float *sx;
     int8_t *cx;
@@ -140,6 +143,7 @@ inline size_t carve(char *base, int64_t M, int64_t K, bool with_codes, bool deco
         ws->sets = reinterpret_cast<uint32_t *>(tg);
         ws->calls = hdr ? reinterpret_cast<uint32_t *>(hdr + 24) : nullptr;
         ws->arrivals = hdr ? reinterpret_cast<unsigned long long *>(hdr + 32) : nullptr;
+        ws->grown = hdr ? reinterpret_cast<uint32_t *>(hdr + 40) : nullptr;
         ws->col_idx = reinterpret_cast<int32_t *>(ci);
         ws->sx = reinterpret_cast<float *>(sx);
         ws->cx = reinterpret_cast<int8_t *>(cx);

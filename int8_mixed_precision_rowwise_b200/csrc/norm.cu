@@ -27,47 +27,71 @@ namespace {
 constexpr int kVec = 4;             // 16-byte vectors a thread holds of its row
 constexpr int kMaxRowThreads = 1024; // so rows of up to 32768 columns stay in registers
 
-// h = x + residual in fp32, rounded once.
+// h = x + residual, rounded once (what an fp32 sum rounded to 16 bits gives as
+// well: 24 bits are enough for the second rounding to change nothing).
 template <bool BF16>
 __device__ __forceinline__ uint4 add8(const uint4 &x, const uint4 &r)
 {
-    const uint32_t *a = reinterpret_cast<const uint32_t *>(&x), *b = reinterpret_cast<const uint32_t *>(&r);
     uint4 o;
-    uint32_t *p = reinterpret_cast<uint32_t *>(&o);
+    if (BF16) {
+        const __nv_bfloat162 *a = reinterpret_cast<const __nv_bfloat162 *>(&x);
+        const __nv_bfloat162 *b = reinterpret_cast<const __nv_bfloat162 *>(&r);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float2 u = up2<BF16>(a[i]), v = up2<BF16>(b[i]);
-        p[i] = down2<BF16>(u.x + v.x, u.y + v.y);
+        for (int i = 0; i < 4; ++i)
+            reinterpret_cast<__nv_bfloat162 *>(&o)[i] = __hadd2(a[i], b[i]);
+    } else {
+        const __half2 *a = reinterpret_cast<const __half2 *>(&x), *b = reinterpret_cast<const __half2 *>(&r);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            reinterpret_cast<__half2 *>(&o)[i] = __hadd2(a[i], b[i]);
     }
     return o;
 }
 
+// Two fp32 values side by side: one instruction a pair.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b)
+{
+    float2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;"
+        : "=l"(reinterpret_cast<uint64_t &>(r))
+        : "l"(reinterpret_cast<uint64_t &>(a)), "l"(reinterpret_cast<uint64_t &>(b)));
+    return r;
+}
+
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
+{
+    float2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;"
+        : "=l"(reinterpret_cast<uint64_t &>(r))
+        : "l"(reinterpret_cast<uint64_t &>(a)), "l"(reinterpret_cast<uint64_t &>(b)),
+          "l"(reinterpret_cast<uint64_t &>(c)));
+    return r;
+}
+
 template <bool BF16>
-__device__ __forceinline__ float squares8(const uint4 &h)
+__device__ __forceinline__ void squares8(const uint4 &h, float2 &sum)
 {
     const uint32_t *a = reinterpret_cast<const uint32_t *>(&h);
-    float s0 = 0.f, s1 = 0.f;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const float2 u = up2<BF16>(a[i]);
-        s0 = fmaf(u.x, u.x, s0);
-        s1 = fmaf(u.y, u.y, s1);
+        sum = fma2(u, u, sum);
     }
-    return s0 + s1;
 }
 
 // y = fp16(h * w * rstd). The product of two 16-bit values is exact in fp32
-// (at most 22 significant bits), so y is off by rstd's rounding and one more.
+// (at most 22 significant bits), so y is off by rstd's error and one rounding.
 template <bool BF16>
 __device__ __forceinline__ uint4 norm8(const uint4 &h, const uint4 &w, float rstd)
 {
     const uint32_t *a = reinterpret_cast<const uint32_t *>(&h), *b = reinterpret_cast<const uint32_t *>(&w);
+    const float2 f = make_float2(rstd, rstd);
     uint4 o;
     uint32_t *p = reinterpret_cast<uint32_t *>(&o);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const float2 u = up2<BF16>(a[i]), v = up2<BF16>(b[i]);
-        p[i] = down2<false>(u.x * v.x * rstd, u.y * v.y * rstd);
+        const float2 y = mul2(mul2(up2<BF16>(a[i]), up2<BF16>(b[i])), f);
+        p[i] = down2<false>(y.x, y.y);
     }
     return o;
 }
@@ -106,9 +130,9 @@ struct NormParams {
     float *absmax;
     int64_t rows;
     int cols;
-    float eps;
+    float eps, inv_cols;
     __half t16;
-    uint32_t *sets, *calls, *sync, *bitmap_out, *status;
+    uint32_t *sets, *calls, *sync, *grown, *bitmap_out, *status;
 };
 
 constexpr int kListed = 1024; // outlier columns that the fix-up visits one by one
@@ -155,46 +179,75 @@ __device__ __forceinline__ int complete_set(const NormParams &p, uint32_t call, 
     return count;
 }
 
-// One warp puts a row right that was coded before the set was complete: its
-// codes in the set's columns become 0, and if its absmax was attained in one
-// of them it is coded again. All other codes stand: a row's absmax and codes
-// depend on the set only through those columns.
-__device__ __forceinline__ void fix_row(const NormParams &p, int64_t r, int count, const uint32_t *s_set,
-                                        const int *s_col)
+// Outlier columns of a vector into the set; a column that is new to it moves
+// the growth counter on (after the set: who reads the counter and then the set
+// sees the column).
+__device__ __forceinline__ void add_hits(const NormParams &p, uint32_t *set, int c, uint32_t hit)
 {
-    const int lane = threadIdx.x & 31, nvec = p.cols >> 3;
-    const __half *Y = reinterpret_cast<const __half *>(p.y) + r * p.cols;
-    int8_t *codes = reinterpret_cast<int8_t *>(p.codes) + r * p.cols;
-    const float old = p.absmax[r], t = __half2float(p.t16);
-    bool stale = count > kListed;
-    if (!stale)
-        for (int i = lane; i < count; i += 32) {
-            const int c = s_col[i];
-            const float a = fabsf(__half2float(Y[c]));
-            if (a < t && codes[c] != 0) {
-                codes[c] = 0;
-                stale |= a == old;
-            }
+    const uint32_t bits = hit << ((c & 3) * 8);
+    if ((atomicOr(set + (c >> 2), bits) & bits) != bits) {
+        __threadfence();
+        atomicAdd(p.grown, 1u);
+    }
+}
+
+// Rows first, first + gridDim.x, .. < end of this CTA were coded before the
+// set was complete. Their codes in the set's columns become 0, and a row whose
+// absmax was attained in one of them is coded again, by the whole CTA. All
+// other codes stand: a row's absmax and codes depend on the set only through
+// those columns. A warp looks at a row's listed columns.
+__device__ __forceinline__ void fix_rows(const NormParams &p, int64_t first, int64_t end, int count,
+                                         const uint32_t *s_set, const int *s_col, float *s_max)
+{
+    __shared__ int s_stale[32];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nwarps = blockDim.x >> 5, nvec = p.cols >> 3;
+    const float t = __half2float(p.t16);
+    for (int64_t r0 = first; r0 < end; r0 += (int64_t)nwarps * gridDim.x) {
+        const int64_t mine = r0 + (int64_t)warp * gridDim.x;
+        if (mine < end) {
+            const __half *Y = reinterpret_cast<const __half *>(p.y) + mine * p.cols;
+            int8_t *codes = reinterpret_cast<int8_t *>(p.codes) + mine * p.cols;
+            const float old = p.absmax[mine];
+            bool stale = count > kListed;
+            if (!stale)
+                for (int i = lane; i < count; i += 32) {
+                    const int c = s_col[i];
+                    const float a = fabsf(__half2float(Y[c]));
+                    if (a < t && codes[c] != 0) {
+                        codes[c] = 0;
+                        stale |= a == old;
+                    }
+                }
+            stale = __any_sync(0xffffffffu, stale);
+            if (lane == 0)
+                s_stale[warp] = stale;
         }
-    if (!__any_sync(0xffffffffu, stale))
-        return;
-    const uint4 *yr = p.y + r * nvec;
-    __half2 m2 = __float2half2_rn(0.f);
-    for (int c = lane; c < nvec; c += 32) {
-        uint4 v = yr[c];
-        mask_known(v, (s_set[c >> 2] >> ((c & 3) * 8)) & 0xFFu);
-        __half2 a[4];
-        m2 = __hmax2(m2, vec_abs_max(v, a));
+        __syncthreads();
+        for (int w = 0; w < nwarps; ++w) {
+            const int64_t r = r0 + (int64_t)w * gridDim.x;
+            if (r >= end || !s_stale[w])
+                continue;
+            const uint4 *yr = p.y + r * nvec;
+            __half2 m2 = __float2half2_rn(0.f);
+            for (int c = tid; c < nvec; c += blockDim.x) {
+                uint4 v = yr[c];
+                mask_known(v, (s_set[c >> 2] >> ((c & 3) * 8)) & 0xFFu);
+                __half2 a[4];
+                m2 = __hmax2(m2, vec_abs_max(v, a));
+            }
+            const float amax = block_all<true>(fmaxf(__low2float(m2), __high2float(m2)), s_max, nwarps);
+            const float s = amax > 0.f ? __fdiv_rn(127.0f, amax) : 0.f;
+            for (int c = tid; c < nvec; c += blockDim.x) {
+                uint4 v = yr[c];
+                mask_known(v, (s_set[c >> 2] >> ((c & 3) * 8)) & 0xFFu);
+                p.codes[r * nvec + c] = codes8(v, s);
+            }
+            if (tid == 0)
+                p.absmax[r] = amax;
+            __syncthreads(); // s_max is free
+        }
+        __syncthreads(); // and s_stale
     }
-    const float amax = warp_all<true>(fmaxf(__low2float(m2), __high2float(m2)));
-    const float s = amax > 0.f ? __fdiv_rn(127.0f, amax) : 0.f;
-    for (int c = lane; c < nvec; c += 32) {
-        uint4 v = yr[c];
-        mask_known(v, (s_set[c >> 2] >> ((c & 3) * 8)) & 0xFFu);
-        p.codes[r * nvec + c] = codes8(v, s);
-    }
-    if (lane == 0)
-        p.absmax[r] = amax;
 }
 
 // One CTA per row, the row in registers from its one read to its codes. With
@@ -217,12 +270,15 @@ __global__ void __launch_bounds__(MAXT, 1024 / MAXT) k_norm_quant(const NormPara
         call = *reinterpret_cast<volatile uint32_t *>(p.calls);
         set = p.sets + (call & 1u) * kSetWords;
     }
+    const __half2 t2 = __half2half2(p.t16);
     uint4 v[kVec];
     float amax = 0.f;
+    uint32_t known = 0u; // outlier columns of this thread's vectors, a byte each
+    uint32_t grown = 0u; // thread 0: the growth counter, and the first row that was
+    int64_t since = -1;  // coded against the set it stands for
     int64_t r = blockIdx.x;
-    for (; r < p.rows; r += gridDim.x) {
+    for (int n = 0; r < p.rows; r += gridDim.x, ++n) {
         const uint4 *xr = p.x + r * nvec;
-        uint32_t known[kVec];
 #pragma unroll
         for (int i = 0; i < kVec; ++i) {
             const int c = tid + i * blockDim.x;
@@ -240,23 +296,40 @@ __global__ void __launch_bounds__(MAXT, 1024 / MAXT) k_norm_quant(const NormPara
             for (int i = 0; i < kVec; ++i)
                 v[i] = add8<BF16>(v[i], u[i]);
         }
-        if (THR) {
+        // Most columns are found by the first rows: look often then, and later
+        // now and again.
+        if (THR && n > 0 && (n < 4 || (n & 7) == 0)) {
+            if (tid == 0) {
+                const uint32_t now = *reinterpret_cast<volatile uint32_t *>(p.grown);
+                if (now != grown || since < 0) {
+                    grown = now;
+                    since = r;
+                }
+                __threadfence();
+            }
+            __syncthreads(); // the counter is read before the set
 #pragma unroll
             for (int i = 0; i < kVec; ++i) {
                 const int c = tid + i * blockDim.x;
-                known[i] = c < nvec ? (__ldcg(set + (c >> 2)) >> ((c & 3) * 8)) & 0xFFu : 0u;
+                if (c < nvec)
+                    known |= ((__ldcg(set + (c >> 2)) >> ((c & 3) * 8)) & 0xFFu) << (8 * i);
             }
         }
-        float ss = 0.f;
+        float2 ss2 = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int i = 0; i < kVec; ++i) {
-            const int c = tid + i * blockDim.x;
-            if (p.h && c < nvec)
-                p.h[r * nvec + c] = v[i];
-            ss += squares8<BF16>(v[i]);
+        for (int i = 0; i < kVec; ++i)
+            squares8<BF16>(v[i], ss2);
+        const float ss = block_all<false>(ss2.x + ss2.y, s_red[0], nwarps);
+        const float rstd = rsqrtf(fmaf(ss, p.inv_cols, p.eps));
+        if (p.h) {
+            uint4 *hr = p.h + r * nvec;
+#pragma unroll
+            for (int i = 0; i < kVec; ++i) {
+                const int c = tid + i * blockDim.x;
+                if (c < nvec)
+                    hr[c] = v[i];
+            }
         }
-        ss = block_all<false>(ss, s_red[0], nwarps);
-        const float rstd = 1.0f / sqrtf(ss / (float)p.cols + p.eps);
         __half2 m2 = __float2half2_rn(0.f);
 #pragma unroll
         for (int i = 0; i < kVec; ++i) {
@@ -268,14 +341,15 @@ __global__ void __launch_bounds__(MAXT, 1024 / MAXT) k_norm_quant(const NormPara
                 __half2 a[4];
                 __half2 m = vec_abs_max(v[i], a);
                 if (THR) {
-                    if (__hge(__hmax(__low2half(m), __high2half(m)), p.t16)) {
+                    // a new column is rare, a known one in few vectors
+                    if (!__hblt2(m, t2)) { // some |y| >= t
                         const uint32_t hit = hit_mask8(v[i], p.t16);
-                        if (hit & ~known[i])
-                            atomicOr(set + (c >> 2), hit << ((c & 3) * 8));
-                        known[i] |= hit;
+                        if (hit & ~(known >> (8 * i)))
+                            add_hits(p, set, c, hit);
+                        known |= hit << (8 * i);
                     }
-                    if (known[i]) {
-                        mask_known(v[i], known[i]);
+                    if ((known >> (8 * i)) & 0xFFu) {
+                        mask_known(v[i], (known >> (8 * i)) & 0xFFu);
                         m = vec_abs_max(v[i], a);
                     }
                 }
@@ -295,7 +369,7 @@ __global__ void __launch_bounds__(MAXT, 1024 / MAXT) k_norm_quant(const NormPara
     }
     if (THR) {
         uint32_t *s_set = s_dyn;
-        int *s_col = reinterpret_cast<int *>(s_dyn + ((p.cols + 31) >> 5));
+        int *s_col = reinterpret_cast<int *>(s_set + ((p.cols + 31) >> 5));
         const int count = complete_set(p, call, s_set, s_col);
         if (count <= 0)
             return;
@@ -326,8 +400,11 @@ __global__ void __launch_bounds__(MAXT, 1024 / MAXT) k_norm_quant(const NormPara
             if (tid == 0)
                 p.absmax[r] = amax;
         }
-        for (int64_t k = blockIdx.x + (int64_t)(tid >> 5) * gridDim.x; k < r; k += (int64_t)nwarps * gridDim.x)
-            fix_row(p, k, count, s_set, s_col);
+        __shared__ int64_t s_since;
+        if (tid == 0) // the counter no longer moves
+            s_since = since >= 0 && *reinterpret_cast<volatile uint32_t *>(p.grown) == grown ? min(since, r) : r;
+        __syncthreads();
+        fix_rows(p, blockIdx.x, s_since, count, s_set, s_col, s_red[0]);
     }
 }
 
@@ -337,7 +414,7 @@ template <bool BF16, bool THR>
 __global__ void __launch_bounds__(kMaxRowThreads, 1) k_norm_quant_wide(const NormParams p)
 {
     __shared__ float s_red[2][32];
-    extern __shared__ uint32_t s_dyn[];
+    extern __shared__ uint32_t s_words[];
     const int tid = threadIdx.x, nwarps = blockDim.x >> 5;
     const int nvec = p.cols >> 3;
     griddep_wait();
@@ -348,7 +425,7 @@ __global__ void __launch_bounds__(kMaxRowThreads, 1) k_norm_quant_wide(const Nor
         set = p.sets + (call & 1u) * kSetWords;
     }
     for (int64_t r = blockIdx.x; r < p.rows; r += gridDim.x) {
-        float ss = 0.f;
+        float2 ss2 = make_float2(0.f, 0.f);
         auto hidden = [&](int c) {
             uint4 v = p.x[r * nvec + c];
             if (p.res)
@@ -356,9 +433,9 @@ __global__ void __launch_bounds__(kMaxRowThreads, 1) k_norm_quant_wide(const Nor
             return v;
         };
         for (int c = tid; c < nvec; c += blockDim.x)
-            ss += squares8<BF16>(hidden(c));
-        ss = block_all<false>(ss, s_red[0], nwarps);
-        const float rstd = 1.0f / sqrtf(ss / (float)p.cols + p.eps);
+            squares8<BF16>(hidden(c), ss2);
+        const float ss = block_all<false>(ss2.x + ss2.y, s_red[0], nwarps);
+        const float rstd = rsqrtf(fmaf(ss, p.inv_cols, p.eps));
         __half2 m2 = __float2half2_rn(0.f);
         for (int c = tid; c < nvec; c += blockDim.x) {
             uint4 v = norm8<BF16>(hidden(c), __ldg(p.w + c), rstd);
@@ -366,7 +443,7 @@ __global__ void __launch_bounds__(kMaxRowThreads, 1) k_norm_quant_wide(const Nor
             if (THR) {
                 const uint32_t hit = hit_mask8(v, p.t16);
                 if (hit) {
-                    atomicOr(set + (c >> 2), hit << ((c & 3) * 8));
+                    add_hits(p, set, c, hit);
                     mask_known(v, hit);
                 }
             }
@@ -391,13 +468,11 @@ __global__ void __launch_bounds__(kMaxRowThreads, 1) k_norm_quant_wide(const Nor
             p.absmax[r] = amax;
     }
     if (THR) {
-        uint32_t *s_set = s_dyn;
-        int *s_col = reinterpret_cast<int *>(s_dyn + ((p.cols + 31) >> 5));
+        uint32_t *s_set = s_words;
+        int *s_col = reinterpret_cast<int *>(s_words + ((p.cols + 31) >> 5));
         const int count = complete_set(p, call, s_set, s_col);
         if (count > 0)
-            for (int64_t k = blockIdx.x + (int64_t)(tid >> 5) * gridDim.x; k < p.rows;
-                 k += (int64_t)nwarps * gridDim.x)
-                fix_row(p, k, count, s_set, s_col);
+            fix_rows(p, blockIdx.x, p.rows, count, s_set, s_col, s_red[0]);
     }
 }
 
@@ -438,10 +513,12 @@ cudaError_t launch_norm_quant(const NormArgs &a, const Workspace &ws, const Devi
     p.rows = a.rows;
     p.cols = (int)a.cols;
     p.eps = a.eps;
+    p.inv_cols = (float)(1.0 / (double)a.cols);
     p.t16 = threshold_fp16(a.t);
     p.sets = ws.sets;
     p.calls = ws.calls;
     p.sync = ws.sync;
+    p.grown = ws.grown;
     p.bitmap_out = a.bitmap;
     p.status = ws.status;
     const int nvec = p.cols >> 3;
@@ -456,21 +533,10 @@ cudaError_t launch_norm_quant(const NormArgs &a, const Workspace &ws, const Devi
         {{k_norm_quant_wide<false, false>, k_norm_quant_wide<false, true>},
          {k_norm_quant_wide<true, false>, k_norm_quant_wide<true, true>}}};
     const Kernel kern = kernels[size][a.bf16][thr];
+    // As many CTAs an SM as their registers (at most 64 a thread) leave room
+    // for: the grid barrier needs them all resident.
+    const int per_sm = size == 2 ? 1 : std::max(1, std::min(1024 / threads, 16));
     const size_t smem = thr ? ((size_t)(p.cols + 31) / 32 + kListed) * 4 : 0;
-    // The grid barrier needs every CTA resident: as many as fit, asked once
-    // per variant and CTA size (at the largest shared memory the variant uses).
-    static std::atomic<int> resident[64][3][2][2][kMaxRowThreads / 32 + 1];
-    std::atomic<int> &fit = resident[dev.device & 63][size][a.bf16][thr][threads / 32];
-    int per_sm = fit.load();
-    if (per_sm == 0) {
-        const size_t most = thr ? (std::min<size_t>(kSetWords, size == 2 ? kSetWords : kMaxRowThreads * kVec / 4) + kListed) * 4 : 0;
-        cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, threads, most);
-        if (e != cudaSuccess)
-            return e;
-        if (per_sm < 1)
-            return cudaErrorLaunchOutOfResources;
-        fit.store(per_sm);
-    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)std::min<int64_t>(a.rows, (int64_t)dev.num_sms * per_sm));
     cfg.blockDim = dim3((unsigned)threads);
