@@ -17,7 +17,7 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 LIB = os.path.join(HERE, "libllmint8.so")
 SOURCES = ["api.cu", "quantize.cu", "gemm.cu", "decode.cu", "tp.cu", "noalloc.cu", "norm.cu", "kvcache.cu",
-           "attention.cu", "attn_decode.cu"]
+           "attention.cu", "attn_decode.cu", "attn_prefill.cu"]
 HEADERS = ["internal.h", "ptx.cuh", "common.cuh", "sched.h", "kvcache.cuh", "attention.cuh"]
 
 NVCC_FLAGS = [

@@ -6,6 +6,8 @@
 //
 // over the keys j <= pos_i (causal) or all of the sequence's, with codes kc,
 // vc and one absmax ka, va per (page, head).
+#include <algorithm>
+
 #include "attention.cuh"
 
 namespace llmint8 {
@@ -27,11 +29,27 @@ cudaError_t launch_kv_attention(const llmint8_kv_cache &c, const AttnArgs &a, co
     p.lse = a.lse;
     p.causal = a.causal ? 1 : 0;
     p.bf16 = a.bf16 ? 1 : 0;
-    p.rows_from = 1;
-    p.rows_to = INT32_MAX;
     p.slots = ws.attn_slots;
     p.arrived = ws.attn_arrived;
-    return launch_attn_decode(p, c, a.max_new * p.group <= 8, dev, stream);
+    // A sequence's rows (new tokens x heads of a group) decide: up to 16 go to
+    // the kernel that streams the cache once for them, more to the one that
+    // fills tensor core tiles of 256. The lengths are on the device, so a batch
+    // that may hold both kinds gets both launches, and each takes its own.
+    // (Without a bound, as many rows as sequences are taken for one each.) A
+    // bound that is wrong costs time only: a kernel that is alone takes all.
+    const int64_t bound = a.max_new > 0 ? std::min(a.max_new, a.tokens) : a.tokens <= c.batch ? 1 : a.tokens;
+    const int64_t most = bound * p.group;
+    const bool few = most <= kAttnFewRows;
+    if (few || c.batch > 1) {
+        p.rows_from = 1;
+        p.rows_to = few ? INT32_MAX : kAttnFewRows;
+        cudaError_t e = launch_attn_decode(p, c, most <= 8, dev, stream);
+        if (e != cudaSuccess || few)
+            return e;
+    }
+    p.rows_from = c.batch > 1 ? kAttnFewRows + 1 : 1;
+    p.rows_to = INT32_MAX;
+    return launch_attn_prefill(p, c, dev, stream);
 }
 
 } // namespace llmint8

@@ -84,11 +84,6 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t v)
     return r;
 }
 
-__device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes)
-{
-    asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
-}
-
 __device__ __forceinline__ uint4 lds128(uint32_t a)
 {
     uint4 v;
@@ -103,83 +98,12 @@ __device__ __forceinline__ uint2 lds64(uint32_t a)
     return v;
 }
 
-// Keys [t0, t1), chunks [c0, c1) of an item: sequence b, head h, row tile r.
-struct Seg {
-    int b, h, r;
-    int row0, rows;    // rows of the tile, of n * group
-    int n, len, keys;  // of the sequence
-    int t0, t1;
-    int c0, c1, chunks;
-};
-
-// The segments of units [u, u1), one after the other.
-template <int TR>
-struct Walk {
-    const AttnParams *p;
-    int64_t u, u1;
-    int b, h, r, c;
-    SeqShape s;
-
-    __device__ __forceinline__ void start(const AttnParams &params, int64_t u0, int64_t end, int b0, int64_t off)
-    {
-        p = &params;
-        u = u0;
-        u1 = end;
-        b = b0;
-        if (u >= u1)
-            return;
-        s = seq_shape(params, b);
-        c = (int)(off % s.chunks);
-        off /= s.chunks;
-        r = (int)(off % s.tiles);
-        h = (int)(off / s.tiles);
-    }
-    __device__ __forceinline__ bool next(Seg &g)
-    {
-        if (u >= u1)
-            return false;
-        if (c == s.chunks) {
-            c = 0;
-            if (++r == s.tiles) {
-                r = 0;
-                if (++h == p->c.heads) {
-                    h = 0;
-                    do {
-                        ++b;
-                        s = seq_shape(*p, b);
-                    } while (s.tiles == 0);
-                }
-            }
-        }
-        g.b = b;
-        g.h = h;
-        g.r = r;
-        g.row0 = r * TR;
-        g.rows = min(TR, s.rows - g.row0);
-        g.n = s.n;
-        g.len = s.len;
-        g.keys = s.keys;
-        g.chunks = s.chunks;
-        g.c0 = c;
-        g.c1 = (int)min((int64_t)s.chunks, c + (u1 - u));
-        int keys = s.keys;
-        if (p->causal) // the tile's last row sees the most
-            keys = max(0, min(keys, s.len - s.n + (g.row0 + g.rows - 1) / p->group + 1));
-        g.t0 = min(g.c0 * kUnit, keys);
-        g.t1 = min(g.c1 * kUnit, keys);
-        u += g.c1 - c;
-        c = g.c1;
-        return true;
-    }
-};
-
 template <int D, int NQ, bool ALIBI>
 __global__ void __launch_bounds__(kThreads, 2) k_attn_decode(const __grid_constant__ CUtensorMap km,
                                                              const __grid_constant__ CUtensorMap vm,
                                                              const AttnParams p)
 {
     using L = Smem<D>;
-    constexpr int TR = 8 * NQ;  // rows of a tile
     constexpr bool kLo = NQ == 1;
     constexpr int KS = D / 16;  // k-steps of q . k, and words a lane holds of a key
     constexpr int MT = D / 16;  // m-tiles of w . v
@@ -212,63 +136,23 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_decode(const __grid_consta
     const Range range = my_range<kThreads>(p, s_merge, s_start);
     if (range.u0 >= range.u1)
         return;
-    Walk<TR> walk;
-    Seg q;
-    walk.start(p, range.u0, range.u1, range.b, range.off);
 
     if (warp == kWarps) {
         // ------------------------------------------------ the loads
-        // Lane j looks after group j's keys, lane j + 8 after its values.
         const int group = lane & 7, page_shift = c.page_shift;
         const bool is_v = lane >= 8;
         const int box = page_shift >= 5 ? 32 : 16; // rows a TMA load brings
         const bool loads = lane < 16 && (group * 16) % box == 0;
-        bool more = walk.next(q);
-        int at = more ? q.t0 : 0;
-        struct Unit {
-            bool some;  // there is a unit
-            int page;   // of this lane's group, -1 if none or not wanted
-            bool want;
-            int h, slot;
-            float scale;
-        };
-        // The unit after the last one, its page number requested.
-        auto fetch = [&](Unit &u) {
-            while (more && at >= q.t1) {
-                more = walk.next(q);
-                if (more)
-                    at = q.t0;
-            }
-            u.some = more;
-            u.page = -1;
-            u.want = false;
-            if (!more)
-                return;
-            const int key = at + group * 16;
-            u.want = lane < 16 && key < q.t1;
-            const int j = key >> page_shift;
-            if (u.want && j < c.table_width)
-                u.page = __ldg(c.table + q.b * c.table_stride + j);
-            u.h = q.h;
-            u.slot = key & (c.page_size - 1);
-            at += kUnit;
-        };
-        bool bad = false, failed = false;
-        // Its scale requested, once the page number is there.
-        auto scale = [&](Unit &u) {
-            if (u.want && (unsigned)u.page >= (unsigned)c.pages) {
-                bad = true;
-                u.page = -1;
-            }
-            u.scale = u.page >= 0 ? __ldg((is_v ? c.va : c.ka) + (u.page * c.heads + u.h)) : 0.f;
-        };
-        Unit u0, u1, u2;
-        fetch(u0);
-        fetch(u1);
-        scale(u0);
+        LoadWalk units;
+        units.start(p, range);
+        bool failed = false;
+        UnitLoad u0, u1, u2;
+        units.fetch(p, u0);
+        units.fetch(p, u1);
+        units.scale(p, u0);
         for (int i = 0; u0.some; ++i) {
-            fetch(u2);
-            scale(u1);
+            units.fetch(p, u2);
+            units.scale(p, u1);
             const int s = i % kStages;
             if (i >= kStages && !mbar_wait(empty + s * 8, ((i / kStages) - 1) & 1))
                 failed = true;
@@ -284,22 +168,14 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_decode(const __grid_consta
             if (load)
                 tma_load_2d(ring + (s * 2 + (is_v ? 1 : 0)) * kTile + group * 16 * D, is_v ? &vm : &km, bar, 0,
                             ((u0.page * c.heads + u0.h) << page_shift) + u0.slot);
-            // A group without a page weighs nothing: scale 0, weight 2^-inf.
-            float *meta = s_meta + (s * kGroups + group) * 4;
-            if (lane < 8) {
-                meta[0] = u0.scale * (1.0f / 127.0f) * p.scale_log2;
-            } else if (lane < 16) {
-                const float vs = fmaxf(u0.scale * (1.0f / 127.0f), 1e-30f);
-                meta[1] = u0.page >= 0 ? log2f(vs) : -INFINITY;
-                meta[2] = u0.page >= 0 ? 1.0f / vs : 0.f;
-            }
+            store_meta(s_meta + (s * kGroups + group) * 4, u0, p.scale_log2);
             __syncwarp();
             if (lane == 0)
                 mbar_arrive(bar);
             u0 = u1;
             u1 = u2;
         }
-        if (bad)
+        if (units.bad)
             atomicOr(c.status, LLMINT8_DEV_BAD_PAGE);
         if (failed && lane == 0)
             atomicOr(c.status, LLMINT8_DEV_TIMEOUT_PRODUCER);
@@ -310,7 +186,10 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_decode(const __grid_consta
     const int g = lane >> 2, t = lane & 3;
     int used = 0;
     bool failed = false;
-    while (walk.next(q)) {
+    Walk walk;
+    Seg q;
+    walk.start(p, range);
+    while (walk.next(p, q)) {
         // As an operand this lane holds dimensions t D/4 .. of row g (of each
         // 8); of the scores it has rows 2 t and 2 t + 1.
         uint32_t qb[NQ][KS][2];
@@ -332,7 +211,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_decode(const __grid_consta
                 reinterpret_cast<uint4 *>(w)[v] = live ? __ldg(src + v) : make_uint4(0, 0, 0, 0);
             float f = 1.f;
             if (p.bf16)
-                f = bf16_row_to_f16<2 * KS>(w);
+                f = bf16_to_f16<2 * KS, true>(w);
 #pragma unroll
             for (int k = 0; k < KS; ++k) {
                 qb[i][k][0] = w[2 * k];
@@ -369,12 +248,12 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_decode(const __grid_consta
                     o[i][n][e] = 0.f;
         }
 
-        for (int unit = q.t0; unit < q.t1; unit += kUnit, ++used) {
+        for (int n = q.c0; n < q.c1; ++n, ++used) {
             const int s = used % kStages;
             if (!failed) // one wait that runs out is enough
                 failed = !mbar_wait(full + s * 8, (used / kStages) & 1);
             __syncwarp();
-            const int key = unit + warp * kSub;
+            const int key = n * kUnit + warp * kSub;
             if (key < q.t1) {
                 const uint32_t kb = ring + s * 2 * kTile + warp * kSub * D, vb = kb + kTile;
                 const float4 m0 = *reinterpret_cast<const float4 *>(s_meta + (s * kGroups + 2 * warp) * 4);
@@ -596,14 +475,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_decode(const __grid_consta
                         const float *part = p.slots + ((int64_t)i * 2 + (i == first ? 1 : 0)) * (16 * (D + 2));
                         const float2 ml = __ldcg(reinterpret_cast<const float2 *>(part + 16 * D) + row);
                         const float4 v = __ldcg(reinterpret_cast<const float4 *>(part) + row * (D / 4) + ch);
-                        const float mn = fmaxf(M, ml.x), mu = mn == -INFINITY ? 0.f : mn;
-                        const float fa = exp2_approx(M - mu), fb = exp2_approx(ml.x - mu);
-                        M = mn;
-                        lsum = fmaf(lsum, fa, ml.y * fb);
-                        acc.x = fmaf(acc.x, fa, v.x * fb);
-                        acc.y = fmaf(acc.y, fa, v.y * fb);
-                        acc.z = fmaf(acc.z, fa, v.z * fb);
-                        acc.w = fmaf(acc.w, fa, v.w * fb);
+                        add_part(M, lsum, acc, ml, v);
                     }
                     finish_row<D>(p, out_row, q.h, q.row0 + row, ch, acc, M, lsum);
                 }

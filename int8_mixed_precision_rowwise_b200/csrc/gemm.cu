@@ -1354,23 +1354,6 @@ bool encode_map_i8(CUtensorMap *map, const void *base, int64_t rows, int64_t K, 
     return r == CUDA_SUCCESS;
 }
 
-// Row-major int8 [rows x head_dim] with boxes of whole rows, swizzled by their
-// width (128 or 64 bytes). Not cached: encoding takes less than a lookup's gain.
-bool encode_map_codes(CUtensorMap *map, const void *base, int64_t rows, int head_dim, int box_rows)
-{
-    EncodeTiledFn enc = encode_fn();
-    if (!enc)
-        return false;
-    cuuint64_t dims[2] = {(cuuint64_t)head_dim, (cuuint64_t)rows};
-    cuuint64_t strides[1] = {(cuuint64_t)head_dim};
-    cuuint32_t box[2] = {(cuuint32_t)head_dim, (cuuint32_t)box_rows};
-    cuuint32_t estr[2] = {1, 1};
-    return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides, box, estr,
-               CU_TENSOR_MAP_INTERLEAVE_NONE,
-               head_dim == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 bool make_map_i8(CUtensorMap *map, int device, const void *base, int64_t rows, int64_t K, int box_rows)
 {
     struct Entry {

@@ -16,7 +16,9 @@ namespace llmint8 {
 constexpr int kDecodeMaxM = 32;
 constexpr int kDecodeMaxCtas = 160;
 constexpr int kHeaderBytes = 256;
-constexpr int kAttnMaxCtas = 320; // CTAs of an attention kernel that split the work
+constexpr int kAttnMaxCtas = 320;     // CTAs the attention of few rows is split over
+constexpr int kAttnPrefillCtas = 160; // and that of many
+constexpr int kAttnFewRows = 16;
 constexpr size_t kSetWords = (LLMINT8_MAX_K + 31) / 32; // bitmap words of the widest X
 // Outlier columns whose operands the prefill GEMM's epilogue reads from
 // per-call gathered copies (more columns: it gathers them in place).
@@ -337,9 +339,12 @@ struct AttnArgs {
     void *out;           // [tokens x heads x head_dim]
     float *lse;          // [tokens x heads] or null
 };
-// Floats of the parked parts: two slots a CTA, each 16 rows of values and two
-// statistics.
-inline size_t attn_slot_floats(int64_t head_dim) { return (size_t)kAttnMaxCtas * 2 * 16 * (size_t)(head_dim + 2); }
+// Floats of the parked parts: two slots a CTA, each a tile's rows of values and
+// two statistics.
+inline size_t attn_slot_floats(int64_t head_dim)
+{
+    return (size_t)(head_dim + 2) * 2 * (kAttnPrefillCtas * 256);
+}
 cudaError_t launch_kv_attention(const llmint8_kv_cache &c, const AttnArgs &a, const Workspace &ws,
                                 const DeviceInfo &dev, cudaStream_t stream);
 

@@ -15,8 +15,10 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cstdint>
 
+#include "attention.cuh"
 #include "common.cuh"
 #include "internal.h"
 #include "kvcache.cuh"
@@ -193,6 +195,29 @@ KvView kv_view(const llmint8_kv_cache &c, uint32_t *status)
     v.cu = c.cu_rows;
     v.status = status;
     return v;
+}
+
+bool encode_map_codes(CUtensorMap *map, const void *base, int64_t rows, int head_dim, int box_rows)
+{
+    using Encode = decltype(&cuTensorMapEncodeTiled);
+    static std::atomic<Encode> encode{nullptr};
+    Encode f = encode.load();
+    if (!f) {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            return false;
+        f = reinterpret_cast<Encode>(p);
+        encode.store(f);
+    }
+    cuuint64_t dims[2] = {(cuuint64_t)head_dim, (cuuint64_t)rows};
+    cuuint64_t strides[1] = {(cuuint64_t)head_dim};
+    cuuint32_t box[2] = {(cuuint32_t)head_dim, (cuuint32_t)box_rows};
+    cuuint32_t estr[2] = {1, 1};
+    return f(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, head_dim == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 cudaError_t launch_kv_append(const llmint8_kv_cache &c, const KvRows &rows, uint32_t *status, const DeviceInfo &,
