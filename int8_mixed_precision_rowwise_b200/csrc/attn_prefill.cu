@@ -479,17 +479,36 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_prefill(const __grid_const
                 if (*s_last) {
                     __threadfence();
                     const int rows = info->rows, row0 = info->row0, h = info->h;
-                    for (int x = tid; x < rows * (D / 4); x += 256) {
-                        const int rr = x / (D / 4), ch = x % (D / 4);
-                        float M = -INFINITY, lsum = 0.f;
-                        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+                    // Eight rows at a time, all their loads under way at once.
+                    constexpr int kLanes = D / 4, kStep = 256 / kLanes; // lanes a row takes, rows a step
+                    const int ch = tid % kLanes;
+                    for (int r0 = tid / kLanes; r0 < rows; r0 += 8 * kStep) {
+                        float M[8], lsum[8];
+                        float4 acc[8];
+#pragma unroll
+                        for (int x = 0; x < 8; ++x) {
+                            M[x] = -INFINITY;
+                            lsum[x] = 0.f;
+                            acc[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+                        }
                         for (int k = from; k <= to; ++k) {
                             const float *it = p.slots + ((int64_t)k * 2 + (k == from ? 1 : 0)) * (kRows * (D + 2));
-                            const float2 ml = __ldcg(reinterpret_cast<const float2 *>(it + kRows * D) + rr);
-                            const float4 v = __ldcg(reinterpret_cast<const float4 *>(it) + rr * (D / 4) + ch);
-                            add_part(M, lsum, acc, ml, v);
+                            float2 ml[8];
+                            float4 v[8];
+#pragma unroll
+                            for (int x = 0; x < 8; ++x) {
+                                const int rr = min(r0 + x * kStep, rows - 1);
+                                ml[x] = __ldcg(reinterpret_cast<const float2 *>(it + kRows * D) + rr);
+                                v[x] = __ldcg(reinterpret_cast<const float4 *>(it) + rr * kLanes + ch);
+                            }
+#pragma unroll
+                            for (int x = 0; x < 8; ++x)
+                                add_part(M[x], lsum[x], acc[x], ml[x], v[x]);
                         }
-                        finish_row<D>(p, out_row, h, row0 + rr, ch, acc, M, lsum);
+#pragma unroll
+                        for (int x = 0; x < 8; ++x)
+                            if (r0 + x * kStep < rows)
+                                finish_row<D>(p, out_row, h, row0 + r0 + x * kStep, ch, acc[x], M[x], lsum[x]);
                     }
                 }
                 sync(); // s_last is free
