@@ -336,11 +336,11 @@ __device__ __forceinline__ void code_pairs_to_f16(uint32_t a, uint32_t b, uint32
     out[3] = minus_1152(__byte_perm(y, 0x64646464u, 0x4342));
 }
 
-// bf16 query values of a row (N words, or with QUAD N words in each of the four
-// lanes of a quad) as fp16: scaled by a power of two that puts the largest
+// bf16 query values of a row that LANES neighbouring lanes share, N words each,
+// as fp16: scaled by a power of two that puts the largest
 // below 2^14, so that bf16's 8 significant bits survive down to 2^-30 of it.
 // Returns the factor that undoes the scaling.
-template <int N, bool QUAD>
+template <int LANES, int N>
 __device__ __forceinline__ float bf16_to_f16(uint32_t (&w)[N])
 {
     float top = 0.f;
@@ -349,10 +349,9 @@ __device__ __forceinline__ float bf16_to_f16(uint32_t (&w)[N])
         const float2 f = up2<true>(w[i]);
         top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
     }
-    if (QUAD) {
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-    }
+#pragma unroll
+    for (int o = 1; o < LANES; o <<= 1)
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
     // 2^(13 - exponent(top)), kept where both it and its inverse are normal
     int e = 13 - ((int)(__float_as_uint(top) >> 23) - 127);
     e = max(-126, min(126, e));

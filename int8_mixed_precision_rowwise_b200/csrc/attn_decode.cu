@@ -211,7 +211,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_decode(const __grid_consta
                 reinterpret_cast<uint4 *>(w)[v] = live ? __ldg(src + v) : make_uint4(0, 0, 0, 0);
             float f = 1.f;
             if (p.bf16)
-                f = bf16_to_f16<2 * KS, true>(w);
+                f = bf16_to_f16<4>(w);
 #pragma unroll
             for (int k = 0; k < KS; ++k) {
                 qb[i][k][0] = w[2 * k];

@@ -37,7 +37,7 @@ constexpr int kRows = 256;     // of a tile
 constexpr int kUnit = 128;     // keys
 constexpr int kGroups = 8;     // of 16 keys
 constexpr int kMetaRing = 8;   // units whose scales are kept: more than can be under way
-constexpr float kSlack = 6.f;  // log2 of how far a weight may exceed 1
+constexpr float kMostWeight = 8192.f; // of 128 weights together, before the maximum moves (fp16 holds 65504)
 // Registers a thread of each role; 128 at launch, 2 x 128 x 192 + 128 x 56 +
 // 128 x 72 = 512 x 128.
 constexpr int kRegsRows = 192, kRegsCodes = 56, kRegsLoad = 72;
@@ -288,21 +288,35 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_prefill(const __grid_const
                 m = -INFINITY;
                 l = 0.f;
                 fac = 1.f;
-                const uint4 *src = reinterpret_cast<const uint4 *>(
+                // D / 8 lanes read a row, 32 of a warp's rows in as many steps
+                // as that takes; a row's place comes from the lane that has it.
+                constexpr int kLanes = D / 8, kSteps = kLanes;
+                const uint64_t src = reinterpret_cast<uint64_t>(
                     static_cast<const uint16_t *>(p.q) + (__ldg(c.cu + info->b) + (int64_t)tok) * p.q_token +
                     head * p.q_head);
-                uint32_t w[D / 2];
-#pragma unroll
-                for (int k = 0; k < D / 8; ++k)
-                    reinterpret_cast<uint4 *>(w)[k] = live ? __ldg(src + k) : make_uint4(0, 0, 0, 0);
-                if (p.bf16)
-                    fac = bf16_to_f16<D / 2, false>(w);
                 const uint32_t flip = p.scale_log2 < 0.f ? 0x80008000u : 0u; // scores grow with the products
-                uint8_t *dst = smem + L::Q + sub * NH * kHalf + r * 128;
+                uint4 w[kSteps];
 #pragma unroll
-                for (int k = 0; k < D / 8; ++k)
-                    *reinterpret_cast<uint4 *>(dst + (k / 8) * kHalf + (((k & 7) ^ (r & 7)) << 4)) =
-                        make_uint4(w[4 * k] ^ flip, w[4 * k + 1] ^ flip, w[4 * k + 2] ^ flip, w[4 * k + 3] ^ flip);
+                for (int k = 0; k < kSteps; ++k) {
+                    const int from = k * (32 / kLanes) + lane / kLanes;
+                    const uint64_t at = __shfl_sync(0xffffffffu, src, from);
+                    const bool there = __shfl_sync(0xffffffffu, (int)live, from);
+                    w[k] = there ? __ldg(reinterpret_cast<const uint4 *>(at) + lane % kLanes) : make_uint4(0, 0, 0, 0);
+                }
+#pragma unroll
+                for (int k = 0; k < kSteps; ++k) {
+                    const int of = k * (32 / kLanes) + lane / kLanes; // row of the warp
+                    if (p.bf16) {
+                        const float f = bf16_to_f16<kLanes>(reinterpret_cast<uint32_t (&)[4]>(w[k]));
+                        const float g = __shfl_sync(0xffffffffu, f, (lane % (32 / kLanes)) * kLanes);
+                        if (lane / (32 / kLanes) == k)
+                            fac = g;
+                    }
+                    const int rr = (warp & 3) * 32 + of, ch = lane % kLanes;
+                    *reinterpret_cast<uint4 *>(smem + L::Q + (sub * NH + ch / 8) * kHalf + rr * 128 +
+                                               (((ch & 7) ^ (rr & 7)) << 4)) =
+                        make_uint4(w[k].x ^ flip, w[k].y ^ flip, w[k].z ^ flip, w[k].w ^ flip);
+                }
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0)
@@ -313,76 +327,80 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_prefill(const __grid_const
                 wait(bar(S_FULL + sub), mine & 1);
                 __syncwarp();
                 tc_fence_after();
-                uint32_t s[4][32];
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    tmem_ld_32x32b_x32(t_s + k * 32, s[k]);
-                tmem_wait_ld();
-                // ---- the row's largest exponent. Scores of a group share one
-                // scale; where keys are masked or have a position term the
-                // exponents are formed one by one, scale 1 from there.
+                // Scores of a group share one scale; where keys are masked or
+                // have a position term the exponents are formed one by one,
+                // scale 1 from there.
                 const bool each = ALIBI || key + kUnit - 1 > lim_min;
-                float top = -INFINITY;
-                if (each) {
+                // The maximum so far mostly will do: that none of the weights
+                // is too large shows in their sum. If one is, the scores (still
+                // in tensor memory) are read again and the maximum moves.
+                bool move = first;
+                uint32_t w16[64];
+                float sum_l;
+                for (;;) {
+                    uint32_t s[4][32];
 #pragma unroll
-                    for (int j = 0; j < kGroups; ++j) {
-                        const float4 mt = meta[j];
-                        const float a = mt.x * fac;
+                    for (int k = 0; k < 4; ++k)
+                        tmem_ld_32x32b_x32(t_s + k * 32, s[k]);
+                    tmem_wait_ld();
+                    if (each) {
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) {
-                            uint32_t &v = s[j >> 1][(j & 1) * 16 + e];
-                            const int kk = key + j * 16 + e;
-                            float x = fmaf(__uint_as_float(v), a, mt.y);
-                            if (ALIBI)
-                                x = fmaf(slope, (float)(kk - pos), x);
-                            if (kk > limit)
-                                x = -INFINITY;
-                            v = __float_as_uint(x);
-                            top = fmaxf(top, x);
+                        for (int j = 0; j < kGroups; ++j) {
+                            const float4 mt = meta[j];
+                            const float a = mt.x * fac;
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) {
+                                uint32_t &v = s[j >> 1][(j & 1) * 16 + e];
+                                const int kk = key + j * 16 + e;
+                                float x = fmaf(__uint_as_float(v), a, mt.y);
+                                if (ALIBI)
+                                    x = fmaf(slope, (float)(kk - pos), x);
+                                if (kk > limit)
+                                    x = -INFINITY;
+                                v = __float_as_uint(x);
+                            }
                         }
                     }
-                } else {
+                    if (move) {
+                        float top = -INFINITY;
 #pragma unroll
-                    for (int j = 0; j < kGroups; ++j) {
-                        const float4 mt = meta[j];
-                        float g0 = -INFINITY, g1 = -INFINITY;
+                        for (int j = 0; j < kGroups; ++j) {
+                            const float4 mt = meta[j];
+                            float g0 = -INFINITY, g1 = -INFINITY;
 #pragma unroll
-                        for (int e = 0; e < 16; e += 4) {
-                            const uint32_t *v = &s[j >> 1][(j & 1) * 16 + e];
-                            g0 = max3(g0, __uint_as_float(v[0]), __uint_as_float(v[1]));
-                            g1 = max3(g1, __uint_as_float(v[2]), __uint_as_float(v[3]));
+                            for (int e = 0; e < 16; e += 4) {
+                                const uint32_t *v = &s[j >> 1][(j & 1) * 16 + e];
+                                g0 = max3(g0, __uint_as_float(v[0]), __uint_as_float(v[1]));
+                                g1 = max3(g1, __uint_as_float(v[2]), __uint_as_float(v[3]));
+                            }
+                            g0 = fmaxf(g0, g1);
+                            top = fmaxf(top, each ? g0 : fmaf(g0, mt.x * fac, mt.y));
                         }
-                        top = fmaxf(top, fmaf(fmaxf(g0, g1), mt.x * fac, mt.y));
-                    }
-                }
-                if (__any_sync(0xffffffffu, top > m + kSlack)) {
-                    const float mn = fmaxf(m, top);
-                    const float alpha = mn == -INFINITY ? 1.f : exp2_approx(m - mn);
-                    m = mn;
-                    l *= alpha;
-                    if (!first) { // the sums so far, with all products before complete
-                        wait(bar(O_FULL + sub), (mine - 1) & 1);
-                        __syncwarp();
-                        tc_fence_after();
+                        const float mn = fmaxf(m, top);
+                        const float alpha = mn == -INFINITY ? 1.f : exp2_approx(m - mn);
+                        m = mn;
+                        l *= alpha;
+                        if (!first) { // the sums so far, with all products before complete
+                            wait(bar(O_FULL + sub), (mine - 1) & 1);
+                            __syncwarp();
+                            tc_fence_after();
 #pragma unroll 1
-                        for (int k = 0; k < D / 16; ++k) {
-                            uint32_t o[16];
-                            tmem_ld_32x32b_x16(t_o + k * 16, o);
-                            tmem_wait_ld();
+                            for (int k = 0; k < D / 16; ++k) {
+                                uint32_t o[16];
+                                tmem_ld_32x32b_x16(t_o + k * 16, o);
+                                tmem_wait_ld();
 #pragma unroll
-                            for (int e = 0; e < 16; ++e)
-                                o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-                            tmem_st_32x32b_x16(t_o + k * 16, o);
+                                for (int e = 0; e < 16; ++e)
+                                    o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                                tmem_st_32x32b_x16(t_o + k * 16, o);
+                            }
                         }
                     }
-                }
-                const float mu = m == -INFINITY ? 0.f : m;
+                    const float mu = m == -INFINITY ? 0.f : m;
+                    sum_l = 0.f;
+                    float all = 0.f;
 #pragma unroll
-                for (int h = 0; h < 4; ++h) {
-                    uint32_t w16[16];
-#pragma unroll
-                    for (int jj = 0; jj < 2; ++jj) {
-                        const int j = 2 * h + jj;
+                    for (int j = 0; j < kGroups; ++j) {
                         const float4 mt = meta[j];
                         const float a = each ? 1.f : mt.x * fac, b = each ? -mu : mt.y - mu;
                         const float2 a2 = make_float2(a, a), b2 = make_float2(b, b);
@@ -394,12 +412,20 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_prefill(const __grid_const
                             x.x = exp2_approx(x.x);
                             x.y = exp2_approx(x.y);
                             sum = add2(sum, x);
-                            w16[jj * 8 + e / 2] = down2<false>(x.x, x.y);
+                            w16[j * 8 + e / 2] = down2<false>(x.x, x.y);
                         }
-                        l = fmaf(sum.x + sum.y, mt.z, l);
+                        sum.x += sum.y;
+                        all += sum.x;
+                        sum_l = fmaf(sum.x, mt.z, sum_l);
                     }
-                    tmem_st_32x32b_x16(t_s + h * 16, w16);
+                    if (move || !__any_sync(0xffffffffu, all > kMostWeight))
+                        break;
+                    move = true;
                 }
+                l += sum_l;
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    tmem_st_32x32b_x32(t_s + h * 32, reinterpret_cast<const uint32_t (&)[32]>(w16[h * 32]));
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
@@ -429,31 +455,48 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_prefill(const __grid_const
                 wait(bar(O_FULL + sub), (mine - 1) & 1);
                 __syncwarp();
                 tc_fence_after();
+                // Through the half's query area, free now, a warp its own rows:
+                // 256 bytes of each at a time, so that whole lines are written.
                 const float inv = whole ? (l > 0.f ? 1.0f / l : 0.f) : 1.f;
-                uint4 *out = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.out) + at * D);
+                uint8_t *stage = smem + L::Q + sub * NH * kHalf + (warp & 3) * (NH * kHalf / 4);
+                constexpr int kRowBytes = D * 2, kCh = kRowBytes / 16; // 16-byte pieces of a staged row
+                const uint64_t to = whole ? reinterpret_cast<uint64_t>(static_cast<uint16_t *>(p.out) + at * D)
+                                          : reinterpret_cast<uint64_t>(part + row * D);
+#pragma unroll 1
+                for (int pass = 0; pass < (whole ? 1 : 2); ++pass) {
+#pragma unroll 1
+                    for (int k = 0; k < (whole ? D : D / 2); k += 16) {
+                        uint32_t o[16];
+                        tmem_ld_32x32b_x16(t_o + pass * (D / 2) + k, o);
+                        tmem_wait_ld();
+                        if (whole) {
+                            uint32_t v[8];
 #pragma unroll
-                for (int k = 0; k < D / 32; ++k) {
-                    uint32_t o[32];
-                    tmem_ld_32x32b_x32(t_o + k * 32, o);
-                    tmem_wait_ld();
-                    if (live && whole) {
-#pragma unroll
-                        for (int e = 0; e < 32; e += 8) {
-                            uint32_t v[4];
-#pragma unroll
-                            for (int x = 0; x < 4; ++x) {
-                                const float y = __uint_as_float(o[e + 2 * x]) * inv;
-                                const float z = __uint_as_float(o[e + 2 * x + 1]) * inv;
+                            for (int x = 0; x < 8; ++x) {
+                                const float y = __uint_as_float(o[2 * x]) * inv, z = __uint_as_float(o[2 * x + 1]) * inv;
                                 v[x] = p.bf16 ? down2<true>(y, z) : down2<false>(y, z);
                             }
-                            out[k * 4 + e / 8] = make_uint4(v[0], v[1], v[2], v[3]);
-                        }
-                    } else if (live) {
 #pragma unroll
-                        for (int e = 0; e < 32; e += 4)
-                            reinterpret_cast<uint4 *>(part)[row * (D / 4) + k * 8 + e / 4] =
-                                make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                            for (int x = 0; x < 2; ++x)
+                                *reinterpret_cast<uint4 *>(stage + lane * kRowBytes + (((k / 8 + x) ^ (lane & 7)) << 4)) =
+                                    make_uint4(v[4 * x], v[4 * x + 1], v[4 * x + 2], v[4 * x + 3]);
+                        } else {
+#pragma unroll
+                            for (int x = 0; x < 4; ++x)
+                                *reinterpret_cast<uint4 *>(stage + lane * kRowBytes + (((k / 4 + x) ^ (lane & 7)) << 4)) =
+                                    make_uint4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
+                        }
                     }
+                    __syncwarp();
+#pragma unroll
+                    for (int k = 0; k < kCh; ++k) {
+                        const int of = k * (32 / kCh) + lane / kCh, ch = lane % kCh;
+                        const uint64_t dst = __shfl_sync(0xffffffffu, to, of);
+                        if (__shfl_sync(0xffffffffu, (int)live, of))
+                            *reinterpret_cast<uint4 *>(dst + pass * kRowBytes + ch * 16) =
+                                *reinterpret_cast<const uint4 *>(stage + of * kRowBytes + ((ch ^ (of & 7)) << 4));
+                    }
+                    __syncwarp();
                 }
                 tc_fence_before(); // read before the next segment's products write there
                 if (live && whole && p.lse)
@@ -479,34 +522,35 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_prefill(const __grid_const
                 if (*s_last) {
                     __threadfence();
                     const int rows = info->rows, row0 = info->row0, h = info->h;
-                    // Eight rows at a time, all their loads under way at once.
+                    // Sixteen rows at a time, all their loads under way at once.
                     constexpr int kLanes = D / 4, kStep = 256 / kLanes; // lanes a row takes, rows a step
                     const int ch = tid % kLanes;
-                    for (int r0 = tid / kLanes; r0 < rows; r0 += 8 * kStep) {
-                        float M[8], lsum[8];
-                        float4 acc[8];
+                    constexpr int kAt = 16;
+                    for (int r0 = tid / kLanes; r0 < rows; r0 += kAt * kStep) {
+                        float M[kAt], lsum[kAt];
+                        float4 acc[kAt];
 #pragma unroll
-                        for (int x = 0; x < 8; ++x) {
+                        for (int x = 0; x < kAt; ++x) {
                             M[x] = -INFINITY;
                             lsum[x] = 0.f;
                             acc[x] = make_float4(0.f, 0.f, 0.f, 0.f);
                         }
                         for (int k = from; k <= to; ++k) {
                             const float *it = p.slots + ((int64_t)k * 2 + (k == from ? 1 : 0)) * (kRows * (D + 2));
-                            float2 ml[8];
-                            float4 v[8];
+                            float2 ml[kAt];
+                            float4 v[kAt];
 #pragma unroll
-                            for (int x = 0; x < 8; ++x) {
+                            for (int x = 0; x < kAt; ++x) {
                                 const int rr = min(r0 + x * kStep, rows - 1);
                                 ml[x] = __ldcg(reinterpret_cast<const float2 *>(it + kRows * D) + rr);
                                 v[x] = __ldcg(reinterpret_cast<const float4 *>(it) + rr * kLanes + ch);
                             }
 #pragma unroll
-                            for (int x = 0; x < 8; ++x)
+                            for (int x = 0; x < kAt; ++x)
                                 add_part(M[x], lsum[x], acc[x], ml[x], v[x]);
                         }
 #pragma unroll
-                        for (int x = 0; x < 8; ++x)
+                        for (int x = 0; x < kAt; ++x)
                             if (r0 + x * kStep < rows)
                                 finish_row<D>(p, out_row, h, row0 + r0 + x * kStep, ch, acc[x], M[x], lsum[x]);
                     }
