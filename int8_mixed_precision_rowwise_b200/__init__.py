@@ -13,6 +13,7 @@ Method: the LLM.int8() mixed-precision decomposition described on the page
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 __all__ = [
@@ -145,6 +146,7 @@ def workspace_size(M: int, N: int, K: int) -> int:
 
 # --------------------------------------------------------------------- torch glue
 
+@functools.cache
 def _torch():
     import torch
     return torch
@@ -589,34 +591,72 @@ def gather_column_blocks(blocks, out=None):
 
 TYPE_F16, TYPE_BF16 = 0, 1  # LLMINT8_TYPE_*
 
+# These calls come several times a layer and token, on little data: what they do on
+# the host counts. Tensors are checked with one expression each (the reason is
+# worked out only for one that fails it), the stream and the workspace found
+# without building device objects, the sizes of workspaces remembered.
+
+
+@functools.cache
+def _types():
+    torch = _torch()
+    return {torch.float16: TYPE_F16, torch.bfloat16: TYPE_BF16}
+
 
 def _value_type(t, name):
-    torch = _torch()
-    if t.dtype == torch.float16:
-        return TYPE_F16
-    if t.dtype == torch.bfloat16:
-        return TYPE_BF16
-    raise TypeError(f"{name} must be torch.float16 or torch.bfloat16, got {t.dtype}")
+    kind = _types().get(t.dtype)
+    if kind is None:
+        raise TypeError(f"{name} must be torch.float16 or torch.bfloat16, got {t.dtype}")
+    return kind
 
 
-def _need_like(t, name, dtype, shape, dev):
-    """A contiguous CUDA tensor of this type, shape and device."""
+def _need_like(t, name, dtype, shape, index):
+    """A contiguous tensor of this type and shape on the CUDA device `index`."""
+    if (hasattr(t, "get_device") and t.get_device() == index and t.dtype is dtype and t.shape == shape
+            and t.is_contiguous()):
+        return
     _need_cuda(t, name, dtype)
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {list(shape)}, got {list(t.shape)}")
-    if t.device != dev:
-        raise ValueError(f"{name} is on {t.device}, expected {dev}")
+    raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
 
 
-def _call(where, dev, *args):
-    """An entry point on the current stream of `dev`, whichever device is current."""
+def _index(t, name):
+    """The CUDA device number of a tensor."""
+    index = t.get_device() if hasattr(t, "get_device") else -1
+    if index < 0:
+        raise TypeError(f"{name} must be a CUDA tensor (the library has no CPU path)")
+    return index
+
+
+def _raw_stream(index):
     torch = _torch()
-    if torch.cuda.current_device() == dev.index:
-        st = load()[where](*args, _stream_ptr(dev))
+    get = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return get(index) if get else torch.cuda.current_stream(index).cuda_stream
+
+
+def _workspace(workspace, nbytes, index):
+    """(address, bytes) of the given workspace, or of the one of the device's current stream."""
+    if workspace is None:
+        workspace = _workspaces.get((index, _raw_stream(index)))
+        if workspace is None or workspace.numel() < nbytes:
+            workspace = get_workspace(nbytes, _torch().device("cuda", index))
+    return workspace.data_ptr(), workspace.numel()
+
+
+def _call(where, index, *args):
+    """An entry point on the current stream of device `index`, whichever device is current."""
+    torch = _torch()
+    if torch.cuda.current_device() == index:
+        st = load()[where](*args, _raw_stream(index))
     else:
-        with torch.cuda.device(dev):
-            st = load()[where](*args, _stream_ptr(dev))
-    _check(st, "llmint8" + where)
+        with torch.cuda.device(index):
+            st = load()[where](*args, _raw_stream(index))
+    if st:
+        _check(st, "llmint8" + where)
+
+
+_quantize_workspace_size = functools.lru_cache(maxsize=256)(quantize_workspace_size)
 
 
 def add_rmsnorm_quantize(X, weight, residual=None, eps: float = 1e-6, threshold: float = 0.0, codes=None,
@@ -628,43 +668,41 @@ def add_rmsnorm_quantize(X, weight, residual=None, eps: float = 1e-6, threshold:
     then returned as None). ``residual_out`` may be X or residual; without a residual it is
     X unless given. With find_outlier_cols the results are matmul_codes' inputs."""
     torch = _torch()
-    _need_cuda(X, "X")
+    index = _index(X, "X")
     kind = _value_type(X, "X")
-    if X.dim() != 2:
-        raise ValueError("X must be [rows x cols]")
+    if X.dim() != 2 or not X.is_contiguous():
+        raise ValueError("X must be [rows x cols] and contiguous")
     rows, cols = X.shape
-    dev = X.device
-    _need_like(weight, "weight", X.dtype, (cols,), dev)
+    _need_like(weight, "weight", X.dtype, (cols,), index)
     if residual is not None:
-        _need_like(residual, "residual", X.dtype, (rows, cols), dev)
-    if Y is False and 0 < threshold < float("inf"):
-        raise ValueError("Y is needed with a threshold: the linear takes its outlier columns from it")
+        _need_like(residual, "residual", X.dtype, (rows, cols), index)
     if codes is None:
-        codes = torch.empty((rows, cols), dtype=torch.int8, device=dev)
+        codes = torch.empty_like(X, dtype=torch.int8)
     else:
-        _need_like(codes, "codes", torch.int8, (rows, cols), dev)
+        _need_like(codes, "codes", torch.int8, (rows, cols), index)
     if row_absmax is None:
-        row_absmax = torch.empty(rows, dtype=torch.float32, device=dev)
+        row_absmax = X.new_empty(rows, dtype=torch.float32)
     else:
-        _need_like(row_absmax, "row_absmax", torch.float32, (rows,), dev)
+        _need_like(row_absmax, "row_absmax", torch.float32, (rows,), index)
     if outlier_bitmap is not None:
-        _need_like(outlier_bitmap, "outlier_bitmap", torch.int32, ((cols + 31) // 32,), dev)
+        _need_like(outlier_bitmap, "outlier_bitmap", torch.int32, ((cols + 31) // 32,), index)
     elif threshold > 0:
-        outlier_bitmap = torch.empty((cols + 31) // 32, dtype=torch.int32, device=dev)
+        outlier_bitmap = X.new_empty((cols + 31) // 32, dtype=torch.int32)
     if Y is None:
-        Y = torch.empty((rows, cols), dtype=torch.float16, device=dev)
+        Y = torch.empty_like(X, dtype=torch.float16)
     elif Y is False:
+        if 0 < threshold < float("inf"):
+            raise ValueError("Y is needed with a threshold: the linear takes its outlier columns from it")
         Y = None
     else:
-        _need_like(Y, "Y", torch.float16, (rows, cols), dev)
+        _need_like(Y, "Y", torch.float16, (rows, cols), index)
     if residual_out is not None:
-        _need_like(residual_out, "residual_out", X.dtype, (rows, cols), dev)
+        _need_like(residual_out, "residual_out", X.dtype, (rows, cols), index)
     elif residual is not None:
         residual_out = torch.empty_like(X)
-    ws = workspace if workspace is not None else get_workspace(quantize_workspace_size(rows, cols), dev)
-    _call("_add_rmsnorm_quantize", dev, X.data_ptr(), _ptr(residual), weight.data_ptr(), kind, rows, cols, float(eps),
-          float(threshold), _ptr(residual_out), _ptr(Y), codes.data_ptr(), row_absmax.data_ptr(),
-          _ptr(outlier_bitmap), ws.data_ptr(), ws.numel())
+    _call("_add_rmsnorm_quantize", index, X.data_ptr(), _ptr(residual), weight.data_ptr(), kind, rows, cols, eps,
+          threshold, _ptr(residual_out), _ptr(Y), codes.data_ptr(), row_absmax.data_ptr(), _ptr(outlier_bitmap),
+          *_workspace(workspace, _quantize_workspace_size(rows, cols), index))
     return codes, row_absmax, outlier_bitmap, Y, (X if residual_out is None else residual_out)
 
 
@@ -672,50 +710,51 @@ def dequantize_rowwise(codes, row_absmax, dtype=None, out=None):
     """codes int8 [rows x cols] times row_absmax / 127 as fp16 (or ``dtype``: torch.bfloat16)
     (llmint8_dequantize_rowwise)."""
     torch = _torch()
-    _need_cuda(codes, "codes", torch.int8)
-    if codes.dim() != 2:
-        raise ValueError("codes must be [rows x cols]")
+    index = _index(codes, "codes")
+    if codes.dim() != 2 or codes.dtype is not torch.int8 or not codes.is_contiguous():
+        raise ValueError("codes must be int8 [rows x cols] and contiguous")
     rows, cols = codes.shape
-    dev = codes.device
-    _need_like(row_absmax, "row_absmax", torch.float32, (rows,), dev)
+    _need_like(row_absmax, "row_absmax", torch.float32, (rows,), index)
     if out is None:
-        out = torch.empty((rows, cols), dtype=dtype or torch.float16, device=dev)
+        out = torch.empty_like(codes, dtype=dtype or torch.float16)
     else:
-        _need_like(out, "out", dtype or out.dtype, (rows, cols), dev)
-    _call("_dequantize_rowwise", dev, codes.data_ptr(), row_absmax.data_ptr(), rows, cols, _value_type(out, "out"),
+        _need_like(out, "out", dtype or out.dtype, (rows, cols), index)
+    _call("_dequantize_rowwise", index, codes.data_ptr(), row_absmax.data_ptr(), rows, cols, _value_type(out, "out"),
           out.data_ptr())
     return out
 
 
 def _kv_cache(k_codes, v_codes, k_absmax, v_absmax, page_table, seq_lens, cu_rows):
-    """The llmint8_kv_cache descriptor of checked tensors."""
+    """(llmint8_kv_cache descriptor of checked tensors, device number)."""
     torch = _torch()
-    _need_cuda(k_codes, "k_codes", torch.int8)
-    if k_codes.dim() != 4:
-        raise ValueError("k_codes must be [pages x heads x page_size x head_dim]")
-    pages, heads, page_size, head_dim = k_codes.shape
-    dev = k_codes.device
-    _need_like(v_codes, "v_codes", torch.int8, k_codes.shape, dev)
-    _need_like(k_absmax, "k_absmax", torch.float32, (pages, heads), dev)
-    _need_like(v_absmax, "v_absmax", torch.float32, (pages, heads), dev)
-    if page_table.dim() != 2 or page_table.dtype != torch.int32 or page_table.device != dev:
-        raise ValueError(f"page_table must be int32 [batch x pages of a sequence] on {dev}")
+    index = _index(k_codes, "k_codes")
+    if k_codes.dim() != 4 or k_codes.dtype is not torch.int8 or not k_codes.is_contiguous():
+        raise ValueError("k_codes must be int8 [pages x heads x page_size x head_dim] and contiguous")
+    shape = k_codes.shape
+    pages, heads, page_size, head_dim = shape
+    _need_like(v_codes, "v_codes", torch.int8, shape, index)
+    _need_like(k_absmax, "k_absmax", torch.float32, (pages, heads), index)
+    _need_like(v_absmax, "v_absmax", torch.float32, (pages, heads), index)
+    _index(page_table, "page_table")
+    if page_table.dim() != 2 or page_table.dtype is not torch.int32 or page_table.get_device() != index:
+        raise ValueError(f"page_table must be int32 [batch x pages of a sequence] on cuda:{index}")
     batch, width = page_table.shape
-    stride = page_table.stride(0) if batch > 1 else width
-    if (width > 1 and page_table.stride(1) != 1) or stride < width:
+    stride, step = page_table.stride()
+    if batch < 2:
+        stride = width
+    if (width > 1 and step != 1) or stride < width:
         raise ValueError("page_table's rows must be contiguous and apart")
-    _need_like(seq_lens, "seq_lens", torch.int32, (batch,), dev)
-    _need_like(cu_rows, "cu_rows", torch.int32, (batch + 1,), dev)
+    _need_like(seq_lens, "seq_lens", torch.int32, (batch,), index)
+    _need_like(cu_rows, "cu_rows", torch.int32, (batch + 1,), index)
     return _KvCache(k_codes.data_ptr(), v_codes.data_ptr(), k_absmax.data_ptr(), v_absmax.data_ptr(), pages, heads,
                     page_size, head_dim, batch, width, stride, page_table.data_ptr(), seq_lens.data_ptr(),
-                    cu_rows.data_ptr())
+                    cu_rows.data_ptr()), index
 
 
-def _need_rows(t, name, heads, head_dim, dev):
+def _need_rows(t, name, heads, head_dim, index):
     """Packed rows [tokens x heads x head_dim], fp16 or bf16, the last dimension dense."""
-    torch = _torch()
-    if not isinstance(t, torch.Tensor) or t.device != dev:
-        raise TypeError(f"{name} must be a tensor on {dev}")
+    if _index(t, name) != index:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
     kind = _value_type(t, name)
     if t.dim() != 3 or t.shape[2] != head_dim or (heads is not None and t.shape[1] != heads):
         raise ValueError(f"{name} must be [tokens x {heads or 'heads'} x {head_dim}], got {list(t.shape)}")
@@ -736,14 +775,12 @@ def kv_append(K, V, k_codes, v_codes, k_absmax, v_absmax, page_table, seq_lens, 
     head_dim] with absmax k_absmax, v_absmax fp32 [pages x heads]. Rows cu_rows[b] .. cu_rows[b+1]
     are the last positions of sequence b, whose length with them is seq_lens[b] and whose pages are
     page_table[b] (llmint8_kv_append)."""
-    c = _kv_cache(k_codes, v_codes, k_absmax, v_absmax, page_table, seq_lens, cu_rows)
-    dev = k_codes.device
-    kind = _need_rows(K, "K", c.heads, c.head_dim, dev)
-    if _need_rows(V, "V", c.heads, c.head_dim, dev) != kind or V.shape != K.shape:
+    c, index = _kv_cache(k_codes, v_codes, k_absmax, v_absmax, page_table, seq_lens, cu_rows)
+    kind = _need_rows(K, "K", c.heads, c.head_dim, index)
+    if _need_rows(V, "V", c.heads, c.head_dim, index) != kind or V.shape != K.shape:
         raise ValueError("K and V must have the same type and shape")
-    ws = workspace if workspace is not None else get_workspace(4096, dev)
-    _call("_kv_append", dev, ctypes.byref(c), K.data_ptr(), V.data_ptr(), kind, K.shape[0], *_row_strides(K),
-          *_row_strides(V), ws.data_ptr(), ws.numel())
+    _call("_kv_append", index, ctypes.byref(c), K.data_ptr(), V.data_ptr(), kind, K.shape[0], *_row_strides(K),
+          *_row_strides(V), *_workspace(workspace, 4096, index))
 
 
 def kv_read(k_codes, v_codes, k_absmax, v_absmax, page_table, seq_lens, cu_rows, tokens: int, dtype=None, K=None,
@@ -751,26 +788,27 @@ def kv_read(k_codes, v_codes, k_absmax, v_absmax, page_table, seq_lens, cu_rows,
     """(K, V) [tokens x heads x head_dim], fp16 (or ``dtype``): the cached values of each sequence's
     last cu_rows[b+1] - cu_rows[b] positions as packed rows (llmint8_kv_read)."""
     torch = _torch()
-    c = _kv_cache(k_codes, v_codes, k_absmax, v_absmax, page_table, seq_lens, cu_rows)
-    dev = k_codes.device
+    c, index = _kv_cache(k_codes, v_codes, k_absmax, v_absmax, page_table, seq_lens, cu_rows)
     shape = (int(tokens), c.heads, c.head_dim)
     dtype = dtype or (torch.float16 if K is None else K.dtype)
     if K is None:
-        K = torch.empty(shape, dtype=dtype, device=dev)
+        K = k_codes.new_empty(shape, dtype=dtype)
     else:
-        _need_like(K, "K", dtype, shape, dev)
+        _need_like(K, "K", dtype, shape, index)
     if V is None:
-        V = torch.empty(shape, dtype=dtype, device=dev)
+        V = k_codes.new_empty(shape, dtype=dtype)
     else:
-        _need_like(V, "V", dtype, shape, dev)
-    ws = workspace if workspace is not None else get_workspace(4096, dev)
-    _call("_kv_read", dev, ctypes.byref(c), K.data_ptr(), V.data_ptr(), _value_type(K, "K"), shape[0], ws.data_ptr(),
-          ws.numel())
+        _need_like(V, "V", dtype, shape, index)
+    _call("_kv_read", index, ctypes.byref(c), K.data_ptr(), V.data_ptr(), _value_type(K, "K"), shape[0],
+          *_workspace(workspace, 4096, index))
     return K, V
 
 
 def kv_attention_workspace_size(heads: int, kv_heads: int, head_dim: int) -> int:
     return int(load()["_kv_attention_workspace_size"](heads, kv_heads, head_dim))
+
+
+_attention_workspace_size = functools.lru_cache(maxsize=256)(kv_attention_workspace_size)
 
 
 def kv_attention(Q, k_codes, v_codes, k_absmax, v_absmax, page_table, seq_lens, cu_rows, scale: float | None = None,
@@ -782,25 +820,23 @@ def kv_attention(Q, k_codes, v_codes, k_absmax, v_absmax, page_table, seq_lens, 
     receives log sum exp; ``max_new``, an upper bound of the new tokens of one sequence (0:
     unknown), only helps to choose the kernel (llmint8_kv_attention)."""
     torch = _torch()
-    c = _kv_cache(k_codes, v_codes, k_absmax, v_absmax, page_table, seq_lens, cu_rows)
-    dev = k_codes.device
-    kind = _need_rows(Q, "Q", None, c.head_dim, dev)
-    tokens, heads = Q.shape[0], Q.shape[1]
+    c, index = _kv_cache(k_codes, v_codes, k_absmax, v_absmax, page_table, seq_lens, cu_rows)
+    head_dim = c.head_dim
+    kind = _need_rows(Q, "Q", None, head_dim, index)
+    tokens, heads, _ = shape = Q.shape
     if alibi_slopes is not None:
-        _need_like(alibi_slopes, "alibi_slopes", torch.float32, (heads,), dev)
+        _need_like(alibi_slopes, "alibi_slopes", torch.float32, (heads,), index)
     if out is None:
-        out = torch.empty((tokens, heads, c.head_dim), dtype=Q.dtype, device=dev)
+        out = torch.empty_like(Q) if Q.is_contiguous() else Q.new_empty(shape)
     else:
-        _need_like(out, "out", Q.dtype, Q.shape, dev)
+        _need_like(out, "out", Q.dtype, shape, index)
     if lse is not None:
-        _need_like(lse, "lse", torch.float32, (tokens, heads), dev)
+        _need_like(lse, "lse", torch.float32, (tokens, heads), index)
     if scale is None:
-        scale = c.head_dim ** -0.5
-    if workspace is None:
-        workspace = get_workspace(kv_attention_workspace_size(heads, c.heads, c.head_dim), dev)
-    _call("_kv_attention", dev, ctypes.byref(c), Q.data_ptr(), kind, tokens, heads, *_row_strides(Q),
-          float(scale), int(bool(causal)), _ptr(alibi_slopes), int(max_new), out.data_ptr(), _ptr(lse),
-          workspace.data_ptr(), workspace.numel())
+        scale = head_dim ** -0.5
+    _call("_kv_attention", index, ctypes.byref(c), Q.data_ptr(), kind, tokens, heads, *_row_strides(Q), scale,
+          1 if causal else 0, _ptr(alibi_slopes), max_new, out.data_ptr(), _ptr(lse),
+          *_workspace(workspace, _attention_workspace_size(heads, c.heads, head_dim), index))
     return out
 
 

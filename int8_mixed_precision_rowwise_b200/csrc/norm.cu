@@ -548,7 +548,7 @@ cudaError_t launch_norm_quant(const NormArgs &a, const Workspace &ws, const Devi
     attr[1].id = cudaLaunchAttributeCooperative;
     attr[1].val.cooperative = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = thr ? 2 : 1;
+    cfg.numAttrs = thr && cfg.gridDim.x > 1 ? 2 : 1; // one CTA is resident anyhow
     return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
