@@ -48,18 +48,24 @@ namespace llmint8 {
 namespace {
 
 constexpr int kWarps = 4;             // that compute
-constexpr int kThreads = (kWarps + 1) * 32;
 constexpr int kSub = 32;              // keys a warp takes at once
 constexpr int kUnit = kSub * kWarps;  // keys of a unit
 constexpr int kGroups = kUnit / 16;   // 16 keys lie in one page
-constexpr int kStages = 3;
 constexpr float kSlack = 6.f;         // log2 of how far a weight may exceed 1
 
-template <int D>
+// With row tiles of 8 the registers allow three CTAs an SM, with 16 two; the
+// ring takes what shared memory that leaves (192 KB an SM either way).
+template <int D, int NQ>
 struct Smem {
+    static constexpr int kCtas = NQ == 1 ? 3 : 2;
+    // With 16 rows the computing warps take registers from the loading one,
+    // which for that comes with three idle ones (a warpgroup each; 2 x 128
+    // threads x 128 at launch).
+    static constexpr int kThreads = NQ == 1 ? (kWarps + 1) * 32 : 256;
+    static constexpr int kStages = NQ == 1 ? 2 : 3;
     static constexpr int kTile = kUnit * D; // a unit's codes of one operand
     static constexpr int kRing = kStages * 2 * kTile;
-    static constexpr int kMerge = kWarps * 8 * D * 4;
+    static constexpr int kMerge = kWarps * 4 * D * 4; // 4 rows at a time
     static constexpr int kMeta = kStages * kGroups * 16; // key scale, log2 value scale, 1 / value scale
     static constexpr int kBars = kStages * 2 * 8;
     static constexpr int kStats = kWarps * 16 * 2 * 4;
@@ -99,11 +105,11 @@ __device__ __forceinline__ uint2 lds64(uint32_t a)
 }
 
 template <int D, int NQ, bool ALIBI>
-__global__ void __launch_bounds__(kThreads, 2) k_attn_decode(const __grid_constant__ CUtensorMap km,
-                                                             const __grid_constant__ CUtensorMap vm,
-                                                             const AttnParams p)
+__global__ void __launch_bounds__(Smem<D, NQ>::kThreads, Smem<D, NQ>::kCtas)
+    k_attn_decode(const __grid_constant__ CUtensorMap km, const __grid_constant__ CUtensorMap vm, const AttnParams p)
 {
-    using L = Smem<D>;
+    using L = Smem<D, NQ>;
+    constexpr int kStages = L::kStages;
     constexpr bool kLo = NQ == 1;
     constexpr int KS = D / 16;  // k-steps of q . k, and words a lane holds of a key
     constexpr int MT = D / 16;  // m-tiles of w . v
@@ -133,12 +139,17 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_decode(const __grid_consta
     griddep_release();
 
     // ---- this CTA's units: [U i / G, U (i + 1) / G), G = min(grid, U)
-    const Range range = my_range<kThreads>(p, s_merge, s_start);
+    const Range range = my_range<L::kThreads>(p, s_merge, s_start);
     if (range.u0 >= range.u1)
         return;
 
-    if (warp == kWarps) {
+    if (warp >= kWarps) {
         // ------------------------------------------------ the loads
+        if (NQ > 1) {
+            regs_less<56>();
+            if (warp > kWarps)
+                return;
+        }
         const int group = lane & 7, page_shift = c.page_shift;
         const bool is_v = lane >= 8;
         const int box = page_shift >= 5 ? 32 : 16; // rows a TMA load brings
@@ -183,6 +194,8 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_decode(const __grid_consta
     }
 
     // ---------------------------------------------------- the computation
+    if (NQ > 1)
+        regs_more<200>();
     const int g = lane >> 2, t = lane & 3;
     int used = 0;
     bool failed = false;
@@ -392,63 +405,62 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_decode(const __grid_consta
                 mbar_arrive(empty + s * 8);
         }
 
-        // ---- the four warps' parts into one, 8 rows at a time
+        // ---- the four warps' parts into one: each lane's rows 2 t, then its
+        // rows 2 t + 1, of each 8
         const bool whole = q.c0 == 0 && q.c1 == q.chunks;
         const int64_t out_row = first_row * p.heads;
         float *slot = p.slots + ((int64_t)blockIdx.x * 2 + (q.c0 == 0 ? 1 : 0)) * (16 * (D + 2));
 #pragma unroll
-        for (int i = 0; i < NQ; ++i) {
+        for (int i = 0; i < NQ; ++i)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 float sum = l[i][e];
                 sum += __shfl_xor_sync(0xffffffffu, sum, 4);
                 sum += __shfl_xor_sync(0xffffffffu, sum, 8);
                 sum += __shfl_xor_sync(0xffffffffu, sum, 16);
-                const int row = 2 * t + e;
                 if (g == 0)
-                    s_ml[warp * 16 + row + 8 * i] = make_float2(m[i][e], sum);
+                    s_ml[warp * 16 + 2 * t + e + 8 * i] = make_float2(m[i][e], sum);
                 // 16-byte chunks swizzled by row: rows are a multiple of all banks apart
-                float4 *dst = reinterpret_cast<float4 *>(s_merge + (warp * 8 + row) * D);
+                float4 *dst = reinterpret_cast<float4 *>(s_merge + (warp * 4 + t) * D);
 #pragma unroll
                 for (int n = 0; n < MT; n += 2)
                     dst[(g * (D / 32) + n / 2) ^ t] =
                         make_float4(o[i][n][e], o[i][n][2 + e], o[i][n + 1][e], o[i][n + 1][2 + e]);
-            }
-            named_barrier_sync(1, kWarps * 32);
-            for (int x = tid; x < 8 * D / 4; x += kWarps * 32) {
-                const int rr = x / (D / 4), ch = x % (D / 4), row = rr + 8 * i;
-                if (row >= q.rows)
-                    break;
-                float2 ml[kWarps];
-                float M = -INFINITY;
+                named_barrier_sync(1, kWarps * 32);
+                for (int x = tid; x < 4 * D / 4; x += kWarps * 32) {
+                    const int rr = x / (D / 4), ch = x % (D / 4), row = 2 * rr + e + 8 * i;
+                    if (row >= q.rows)
+                        break;
+                    float2 ml[kWarps];
+                    float M = -INFINITY;
 #pragma unroll
-                for (int w = 0; w < kWarps; ++w) {
-                    ml[w] = s_ml[w * 16 + row];
-                    M = fmaxf(M, ml[w].x);
-                }
-                const float mu = M == -INFINITY ? 0.f : M;
-                float lsum = 0.f;
-                float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+                    for (int w = 0; w < kWarps; ++w) {
+                        ml[w] = s_ml[w * 16 + row];
+                        M = fmaxf(M, ml[w].x);
+                    }
+                    const float mu = M == -INFINITY ? 0.f : M;
+                    float lsum = 0.f;
+                    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-                for (int w = 0; w < kWarps; ++w) {
-                    const float f = exp2_approx(ml[w].x - mu);
-                    const float4 v = reinterpret_cast<const float4 *>(s_merge + (w * 8 + rr) * D)[ch ^ (rr >> 1)];
-                    lsum = fmaf(ml[w].y, f, lsum);
-                    acc.x = fmaf(v.x, f, acc.x);
-                    acc.y = fmaf(v.y, f, acc.y);
-                    acc.z = fmaf(v.z, f, acc.z);
-                    acc.w = fmaf(v.w, f, acc.w);
+                    for (int w = 0; w < kWarps; ++w) {
+                        const float f = exp2_approx(ml[w].x - mu);
+                        const float4 v = reinterpret_cast<const float4 *>(s_merge + (w * 4 + rr) * D)[ch ^ rr];
+                        lsum = fmaf(ml[w].y, f, lsum);
+                        acc.x = fmaf(v.x, f, acc.x);
+                        acc.y = fmaf(v.y, f, acc.y);
+                        acc.z = fmaf(v.z, f, acc.z);
+                        acc.w = fmaf(v.w, f, acc.w);
+                    }
+                    if (whole) {
+                        finish_row<D>(p, out_row, q.h, q.row0 + row, ch, acc, M, lsum);
+                    } else {
+                        reinterpret_cast<float4 *>(slot)[row * (D / 4) + ch] = acc;
+                        if (ch == 0)
+                            reinterpret_cast<float2 *>(slot + 16 * D)[row] = make_float2(M, lsum);
+                    }
                 }
-                if (whole) {
-                    finish_row<D>(p, out_row, q.h, q.row0 + row, ch, acc, M, lsum);
-                } else {
-                    reinterpret_cast<float4 *>(slot)[row * (D / 4) + ch] = acc;
-                    if (ch == 0)
-                        reinterpret_cast<float2 *>(slot + 16 * D)[row] = make_float2(M, lsum);
-                }
+                named_barrier_sync(1, kWarps * 32); // the buffer is free
             }
-            named_barrier_sync(1, kWarps * 32); // the buffer is free
-        }
         if (!whole) {
             // Parts lie in CTA `first` (its opening slot) and all CTAs to
             // `last` (their other slots). The last to arrive adds them.
@@ -495,12 +507,12 @@ cudaError_t launch(const AttnParams &p, const CUtensorMap &km, const CUtensorMap
     static std::atomic<uint64_t> configured[2];
     const uint64_t bit = 1ull << (device & 63);
     if (!(configured[p.slopes ? 1 : 0].load() & bit)) {
-        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D>::kTotal);
+        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D, NQ>::kTotal);
         if (e != cudaSuccess)
             return e;
         configured[p.slopes ? 1 : 0].fetch_or(bit);
     }
-    return launch_pdl(kern, dim3((unsigned)grid), kThreads, Smem<D>::kTotal, stream, km, vm, p);
+    return launch_pdl(kern, dim3((unsigned)grid), Smem<D, NQ>::kThreads, Smem<D, NQ>::kTotal, stream, km, vm, p);
 }
 
 } // namespace
@@ -516,7 +528,7 @@ cudaError_t launch_attn_decode(AttnParams p, const llmint8_kv_cache &c, bool r8,
         return cudaErrorInvalidValue;
     p.tile_rows = r8 ? 8 : 16;
     p.unit = kUnit;
-    const int grid = std::min(kAttnMaxCtas, 2 * dev.num_sms);
+    const int grid = std::min(kAttnMaxCtas, (r8 ? 3 : 2) * dev.num_sms);
     if (c.head_dim == 128)
         return r8 ? launch<128, 1>(p, km, vm, grid, dev.device, stream)
                   : launch<128, 2>(p, km, vm, grid, dev.device, stream);

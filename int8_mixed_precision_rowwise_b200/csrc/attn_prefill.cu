@@ -127,18 +127,6 @@ __device__ __forceinline__ bool elect_one()
     return r != 0;
 }
 
-template <int N>
-__device__ __forceinline__ void regs_more()
-{
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
-}
-
-template <int N>
-__device__ __forceinline__ void regs_less()
-{
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
-}
-
 __device__ __forceinline__ float max3(float a, float b, float c)
 {
     float r;

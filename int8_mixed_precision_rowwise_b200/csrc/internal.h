@@ -16,7 +16,7 @@ namespace llmint8 {
 constexpr int kDecodeMaxM = 32;
 constexpr int kDecodeMaxCtas = 160;
 constexpr int kHeaderBytes = 256;
-constexpr int kAttnMaxCtas = 320;     // CTAs the attention of few rows is split over
+constexpr int kAttnMaxCtas = 480;     // CTAs the attention of few rows is split over
 constexpr int kAttnPrefillCtas = 160; // and that of many
 constexpr int kAttnFewRows = 16;
 constexpr size_t kSetWords = (LLMINT8_MAX_K + 31) / 32; // bitmap words of the widest X
