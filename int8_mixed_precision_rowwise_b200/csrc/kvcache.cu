@@ -61,56 +61,97 @@ struct AppendParams {
     const uint4 *src[2];
     int64_t token[2], head[2]; // strides in 16-byte vectors
     int64_t tokens;
+    int window; // packed tokens a CTA takes
 };
 
-constexpr int kWindow = 16; // packed tokens a CTA looks at
+constexpr int kHeads = 8;   // heads a CTA takes
+constexpr int kWindow = 16; // packed tokens a CTA takes
 
-// A warp takes one (page, head) of the keys or the values: the run of new
-// tokens that starts at a page's first slot or at the sequence's first new
-// token. A CTA covers the runs that start in kWindow packed tokens.
-template <bool BF16, int D>
-__global__ void __launch_bounds__(128) k_kv_append(const AppendParams p)
+// The places of a CTA's packed tokens [t0, t0 + n): page (-1: none), position
+// and the end of the sequence's rows, each found by one lane.
+struct Places {
+    int page[kWindow], slot[kWindow], begin[kWindow], end[kWindow];
+};
+
+__device__ __forceinline__ void find_places(const KvView &c, int64_t t0, int n, int64_t tokens, Places &s)
 {
-    constexpr int kLanes = D / 8;        // lanes a token's row takes
-    constexpr int kRows = 32 / kLanes;   // rows a warp reads at once
+    const int i = threadIdx.x;
+    if (i < kWindow) {
+        int page = -1, slot = 0, begin = 0, end = 0;
+        const int64_t t = t0 + i;
+        const int b = i < n && t < tokens ? sequence_of(c, t) : -1;
+        if (b >= 0) {
+            begin = __ldg(c.cu + b);
+            end = __ldg(c.cu + b + 1);
+            const int64_t pos = (int64_t)__ldg(c.lens + b) - (end - t);
+            if (t >= begin && t < end && pos >= 0) { // offsets that decrease have no rows
+                page = page_of(c, b, (int)pos);
+                slot = (int)pos & (c.page_size - 1);
+            }
+        }
+        s.page[i] = page;
+        s.slot[i] = slot;
+        s.begin[i] = begin;
+        s.end[i] = end;
+    }
+    __syncthreads();
+}
+
+// A warp takes a (page, head) of the keys or the values: the run of new tokens
+// that starts at a page's first slot or at the sequence's first new token. A
+// CTA covers the runs that start in its `window` packed tokens, for kHeads
+// heads; a run of up to 16 tokens is read once, into registers, a longer one
+// (pages of more) a second time, from the caches.
+template <bool BF16, int D>
+__global__ void __launch_bounds__(kHeads * 32, 4) k_kv_append(const AppendParams p)
+{
+    constexpr int kLanes = D / 8;      // lanes a token's row takes
+    constexpr int kRows = 32 / kLanes; // rows a warp reads at once
+    constexpr int kHeld = 16 / kRows;  // vectors of 16 rows in a lane
+    __shared__ Places s;
     const KvView &c = p.c;
-    const int h = blockIdx.y, kv = blockIdx.z;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int h = blockIdx.y * kHeads + warp, kv = blockIdx.z;
     const int row = lane / kLanes, vec = lane % kLanes;
+    const int64_t t0 = (int64_t)blockIdx.x * p.window;
+    const int64_t step = p.token[kv];
+    const uint4 *src = p.src[kv] + (int64_t)h * p.head[kv] + vec;
     griddep_wait();
     griddep_release();
-    const uint4 *src = p.src[kv] + (int64_t)h * p.head[kv] + vec;
-    for (int i = warp; i < kWindow; i += 4) {
-        const int64_t t = (int64_t)blockIdx.x * kWindow + i;
-        if (t >= p.tokens)
-            break;
-        const int b = sequence_of(c, t);
-        if (b < 0)
+    // The window's rows on their way while their places are looked up: most of
+    // them are this CTA's.
+    if (h < c.heads && vec % 8 == 0)
+        for (int r = row; r < p.window && t0 + r < p.tokens; r += kRows)
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(src + (t0 + r) * step));
+    find_places(c, t0, p.window, p.tokens, s);
+    if (h >= c.heads)
+        return;
+    for (int i = 0; i < p.window; ++i) {
+        const int page = s.page[i], slot = s.slot[i];
+        const int64_t t = t0 + i;
+        if (page < 0 || (slot != 0 && t != s.begin[i]))
             continue;
-        const int begin = __ldg(c.cu + b), end = __ldg(c.cu + b + 1);
-        if (t < begin || t >= end)
-            continue; // offsets that decrease
-        const int64_t pos64 = (int64_t)__ldg(c.lens + b) - (end - t);
-        if (pos64 < 0)
-            continue;
-        const int pos = (int)pos64;
-        const int slot = pos & (c.page_size - 1);
-        if (t != begin && slot != 0)
-            continue;
-        const int page = page_of(c, b, pos);
-        if (page < 0)
-            continue;
-        const int n = (int)min((int64_t)min(c.page_size - slot, end - (int)t), p.tokens - t);
-        float amax = 0.f;
-        for (int r = row; r < n; r += kRows)
-            amax = fmaxf(amax, amax8<BF16>(__ldg(src + (t + r) * p.token[kv])));
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1)
-            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+        const int len = (int)min((int64_t)min(c.page_size - slot, s.end[i] - (int)t), p.tokens - t);
         const int64_t block = (int64_t)page * c.heads + h;
         float *scale = (kv ? c.va : c.ka) + block;
         int8_t *dst = (kv ? c.v : c.k) + block * c.page_size * D;
         const float old = slot ? *scale : 0.f;
+        uint4 held[kHeld];
+        float amax = 0.f;
+#pragma unroll
+        for (int k = 0; k < kHeld; ++k) {
+            const int r = row + k * kRows;
+            held[k] = r < len ? __ldg(src + (t + r) * step) : make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int k = 0; k < kHeld; ++k)
+            amax = fmaxf(amax, amax8<BF16>(held[k]));
+#pragma unroll 8
+        for (int r = 16 + row; r < len; r += kRows)
+            amax = fmaxf(amax, amax8<BF16>(__ldg(src + (t + r) * step)));
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
         if (old > amax)
             amax = old;
         if (slot && old < amax) {
@@ -124,53 +165,79 @@ __global__ void __launch_bounds__(128) k_kv_append(const AppendParams p)
                 reinterpret_cast<uint4 *>(dst)[j] = v;
             }
         }
-        const float s = amax > kTinyAbsmax ? __fdiv_rn(127.0f, amax) : 0.f;
-        for (int r = row; r < n; r += kRows)
-            *reinterpret_cast<uint2 *>(dst + (slot + r) * D + vec * 8) =
-                kv_codes8<BF16>(__ldg(src + (t + r) * p.token[kv]), s);
+        const float m = amax > kTinyAbsmax ? __fdiv_rn(127.0f, amax) : 0.f;
+        uint2 *to = reinterpret_cast<uint2 *>(dst + slot * D + vec * 8);
+#pragma unroll
+        for (int k = 0; k < kHeld; ++k) {
+            const int r = row + k * kRows;
+            if (r < len)
+                to[r * (D / 8)] = kv_codes8<BF16>(held[k], m);
+        }
+#pragma unroll 4
+        for (int r = 16 + row; r < len; r += kRows)
+            to[r * (D / 8)] = kv_codes8<BF16>(__ldg(src + (t + r) * step), m);
         __syncwarp();
         if (lane == 0)
             *scale = amax;
     }
 }
 
-// 16 codes a thread.
-template <bool BF16>
-__global__ void __launch_bounds__(256) k_kv_read(const KvView c, uint4 *k_out, uint4 *v_out, int64_t tokens, int d16)
+// kWindow packed tokens of kHeads heads a CTA, 16 codes of a key and of a value
+// a thread and step: tokens of a page lie one after the other.
+template <bool BF16, int D>
+__global__ void __launch_bounds__(256, 4) k_kv_read(const KvView c, uint4 *k_out, uint4 *v_out, int64_t tokens)
 {
+    constexpr int kPieces = D / 16, kSteps = kHeads * kWindow * kPieces / 256;
+    __shared__ Places s;
+    const int64_t t0 = (int64_t)blockIdx.x * kWindow;
     griddep_wait();
     griddep_release();
-    const int64_t per = (int64_t)c.heads * d16;
-    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < tokens * per;
-         i += (int64_t)gridDim.x * blockDim.x) {
-        const int64_t t = i / per;
-        const int e = (int)(i - t * per), h = e / d16, x = e - h * d16;
-        const int b = sequence_of(c, t);
-        if (b < 0)
-            continue;
-        const int begin = __ldg(c.cu + b), end = __ldg(c.cu + b + 1);
-        const int64_t pos = (int64_t)__ldg(c.lens + b) - (end - t);
-        if (t < begin || t >= end || pos < 0)
-            continue;
-        const int page = page_of(c, b, (int)pos);
-        if (page < 0)
-            continue;
-        const int64_t block = (int64_t)page * c.heads + h;
-        const int64_t at = (block * c.page_size + (pos & (c.page_size - 1))) * d16 + x;
+    find_places(c, t0, kWindow, tokens, s);
+    for (int h0 = blockIdx.y * kHeads; h0 < c.heads; h0 += gridDim.y * kHeads) {
+        uint4 v[kSteps][2];
+        float f[kSteps][2];
 #pragma unroll
-        for (int kv = 0; kv < 2; ++kv) {
-            uint4 *out = kv ? v_out : k_out;
-            const uint4 v = __ldg(reinterpret_cast<const uint4 *>(kv ? c.v : c.k) + at);
-            const float s = __fdiv_rn(__ldg((kv ? c.va : c.ka) + block), 127.0f);
-            const int8_t *a = reinterpret_cast<const int8_t *>(&v);
-            uint32_t o[8];
+        for (int i = 0; i < kSteps; ++i) {
+            const int e = threadIdx.x + i * 256, x = e % kPieces, r = e / kPieces % kWindow;
+            const int h = h0 + e / (kPieces * kWindow);
+            if (s.page[r] >= 0 && h < c.heads) {
+                const int64_t block = (int64_t)s.page[r] * c.heads + h;
+                const int64_t at = (block * c.page_size + s.slot[r]) * kPieces + x;
+                v[i][0] = __ldg(reinterpret_cast<const uint4 *>(c.k) + at);
+                v[i][1] = __ldg(reinterpret_cast<const uint4 *>(c.v) + at);
+                f[i][0] = __ldg(c.ka + block);
+                f[i][1] = __ldg(c.va + block);
+            }
+        }
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                o[j] = down2<BF16>((float)a[2 * j] * s, (float)a[2 * j + 1] * s);
-            out[2 * i] = make_uint4(o[0], o[1], o[2], o[3]);
-            out[2 * i + 1] = make_uint4(o[4], o[5], o[6], o[7]);
+        for (int i = 0; i < kSteps; ++i) {
+            const int e = threadIdx.x + i * 256, x = e % kPieces, r = e / kPieces % kWindow;
+            const int h = h0 + e / (kPieces * kWindow);
+            if (s.page[r] >= 0 && h < c.heads) {
+                const int64_t at = (((t0 + r) * c.heads + h) * kPieces + x) * 2;
+#pragma unroll
+                for (int kv = 0; kv < 2; ++kv) {
+                    uint4 *out = (kv ? v_out : k_out) + at;
+                    const float m = __fdiv_rn(f[i][kv], 127.0f);
+                    const int8_t *a = reinterpret_cast<const int8_t *>(&v[i][kv]);
+                    uint32_t o[8];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        o[j] = down2<BF16>((float)a[2 * j] * m, (float)a[2 * j + 1] * m);
+                    out[0] = make_uint4(o[0], o[1], o[2], o[3]);
+                    out[1] = make_uint4(o[4], o[5], o[6], o[7]);
+                }
+            }
         }
     }
+}
+
+// CTAs over the heads' groups: enough for two rounds of three an SM; a CTA
+// that takes more of them looks its tokens up once.
+int head_groups(int64_t windows, int heads, const DeviceInfo &dev)
+{
+    const int64_t groups = (heads + kHeads - 1) / kHeads;
+    return (int)std::max<int64_t>(1, std::min<int64_t>(groups, (6 * dev.num_sms + windows - 1) / windows));
 }
 
 } // namespace
@@ -232,19 +299,25 @@ cudaError_t launch_kv_append(const llmint8_kv_cache &c, const KvRows &rows, uint
     p.head[0] = rows.k_head / 8;
     p.head[1] = rows.v_head / 8;
     p.tokens = rows.tokens;
+    // A step of single tokens has a run in each: one token a CTA, or its warps
+    // would take 16 runs one after the other.
+    p.window = rows.tokens <= 4 * (int64_t)c.batch ? 1 : kWindow;
     auto kern = c.head_dim == 128 ? (rows.bf16 ? k_kv_append<true, 128> : k_kv_append<false, 128>)
                                   : (rows.bf16 ? k_kv_append<true, 64> : k_kv_append<false, 64>);
-    const dim3 grid((unsigned)((rows.tokens + kWindow - 1) / kWindow), (unsigned)c.heads, 2);
-    return launch_pdl(kern, grid, 128, 0, stream, p);
+    const int64_t windows = (rows.tokens + p.window - 1) / p.window;
+    const dim3 grid((unsigned)windows, (unsigned)((c.heads + kHeads - 1) / kHeads), 2);
+    return launch_pdl(kern, grid, kHeads * 32, 0, stream, p);
 }
 
 cudaError_t launch_kv_read(const llmint8_kv_cache &c, void *k, void *v, int64_t tokens, bool bf16, uint32_t *status,
                            const DeviceInfo &dev, cudaStream_t stream)
 {
-    const int64_t n = tokens * c.heads * (c.head_dim / 16);
-    const int64_t grid = std::min<int64_t>((n + 255) / 256, (int64_t)dev.num_sms * 64);
-    return launch_pdl(bf16 ? k_kv_read<true> : k_kv_read<false>, dim3((unsigned)grid), 256, 0, stream,
-                      kv_view(c, status), static_cast<uint4 *>(k), static_cast<uint4 *>(v), tokens, c.head_dim / 16);
+    auto kern = c.head_dim == 128 ? (bf16 ? k_kv_read<true, 128> : k_kv_read<false, 128>)
+                                  : (bf16 ? k_kv_read<true, 64> : k_kv_read<false, 64>);
+    const int64_t windows = (tokens + kWindow - 1) / kWindow;
+    const dim3 grid((unsigned)windows, (unsigned)head_groups(windows, c.heads, dev));
+    return launch_pdl(kern, grid, 256, 0, stream, kv_view(c, status), static_cast<uint4 *>(k), static_cast<uint4 *>(v),
+                      tokens);
 }
 
 } // namespace llmint8
