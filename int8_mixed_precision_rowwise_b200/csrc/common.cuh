@@ -65,6 +65,20 @@ __device__ __forceinline__ uint32_t down2(float a, float b)
     return *reinterpret_cast<const uint32_t *>(&r);
 }
 
+// Four int8 codes (a word) times m, rounded to 16 bits. The codes become fp32
+// without conversions: a code with its sign bit flipped is c + 128, as the low
+// byte of an fp32 in [2^23, 2^24) it is 2^23 + 128 + c.
+template <bool BF16>
+__device__ __forceinline__ uint2 code_values4(uint32_t w, float m)
+{
+    w ^= 0x80808080u;
+    float f[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        f[i] = (__uint_as_float(__byte_perm(w, 0x4B000000u, 0x7440 + i)) - 8388736.f) * m;
+    return make_uint2(down2<BF16>(f[0], f[1]), down2<BF16>(f[2], f[3]));
+}
+
 // Per 16-byte vector (8 fp16 values): |x| as half2 pairs and their maximum.
 __device__ __forceinline__ __half2 vec_abs_max(const uint4 &v, __half2 (&a)[4])
 {

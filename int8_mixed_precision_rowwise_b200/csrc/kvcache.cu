@@ -29,17 +29,11 @@ namespace {
 // Below this absmax 127 / absmax is not finite in fp32: the block's codes are 0.
 constexpr float kTinyAbsmax = 4e-37f;
 
-template <bool BF16>
-__device__ __forceinline__ float amax8(const uint4 &v)
+// Magnitudes of 16-bit floats are in the order of their bits.
+__device__ __forceinline__ uint32_t max_bits8(uint32_t m, const uint4 &v)
 {
-    const uint32_t *a = reinterpret_cast<const uint32_t *>(&v);
-    float m = 0.f;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float2 u = up2<BF16>(a[i]);
-        m = fmaxf(m, fmaxf(fabsf(u.x), fabsf(u.y)));
-    }
-    return m;
+    m = __vmaxu2(__vmaxu2(m, v.x & 0x7FFF7FFFu), __vmaxu2(v.y & 0x7FFF7FFFu, v.z & 0x7FFF7FFFu));
+    return __vmaxu2(m, v.w & 0x7FFF7FFFu);
 }
 
 template <bool BF16>
@@ -126,32 +120,36 @@ __global__ void __launch_bounds__(kHeads * 32, 4) k_kv_append(const AppendParams
     find_places(c, t0, p.window, p.tokens, s);
     if (h >= c.heads)
         return;
-    for (int i = 0; i < p.window; ++i) {
-        const int page = s.page[i], slot = s.slot[i];
+    // The window's tokens that start a run.
+    const bool starts = lane < p.window && s.page[lane % kWindow] >= 0 &&
+                        (s.slot[lane % kWindow] == 0 || t0 + lane == s.begin[lane % kWindow]);
+    for (uint32_t runs = __ballot_sync(0xffffffffu, starts); runs; runs &= runs - 1u) {
+        const int i = __ffs(runs) - 1, page = s.page[i], slot = s.slot[i];
         const int64_t t = t0 + i;
-        if (page < 0 || (slot != 0 && t != s.begin[i]))
-            continue;
         const int len = (int)min((int64_t)min(c.page_size - slot, s.end[i] - (int)t), p.tokens - t);
         const int64_t block = (int64_t)page * c.heads + h;
         float *scale = (kv ? c.va : c.ka) + block;
         int8_t *dst = (kv ? c.v : c.k) + block * c.page_size * D;
         const float old = slot ? *scale : 0.f;
+        const uint4 *rows = src + t * step;
         uint4 held[kHeld];
-        float amax = 0.f;
+        uint32_t bits = 0u;
 #pragma unroll
         for (int k = 0; k < kHeld; ++k) {
             const int r = row + k * kRows;
-            held[k] = r < len ? __ldg(src + (t + r) * step) : make_uint4(0, 0, 0, 0);
+            held[k] = r < len ? __ldg(rows + r * step) : make_uint4(0, 0, 0, 0);
         }
 #pragma unroll
         for (int k = 0; k < kHeld; ++k)
-            amax = fmaxf(amax, amax8<BF16>(held[k]));
+            bits = max_bits8(bits, held[k]);
 #pragma unroll 8
         for (int r = 16 + row; r < len; r += kRows)
-            amax = fmaxf(amax, amax8<BF16>(__ldg(src + (t + r) * step)));
+            bits = max_bits8(bits, __ldg(rows + r * step));
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1)
-            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+            bits = __vmaxu2(bits, __shfl_xor_sync(0xffffffffu, bits, o));
+        const float2 top = up2<BF16>(bits);
+        float amax = fmaxf(top.x, top.y);
         if (old > amax)
             amax = old;
         if (slot && old < amax) {
@@ -175,57 +173,51 @@ __global__ void __launch_bounds__(kHeads * 32, 4) k_kv_append(const AppendParams
         }
 #pragma unroll 4
         for (int r = 16 + row; r < len; r += kRows)
-            to[r * (D / 8)] = kv_codes8<BF16>(__ldg(src + (t + r) * step), m);
+            to[r * (D / 8)] = kv_codes8<BF16>(__ldg(rows + r * step), m);
         __syncwarp();
         if (lane == 0)
             *scale = amax;
     }
 }
 
-// kWindow packed tokens of kHeads heads a CTA, 16 codes of a key and of a value
-// a thread and step: tokens of a page lie one after the other.
+// kWindow packed tokens of kHeads heads a CTA and turn, 8 codes a thread and
+// step: tokens of a page lie one after the other, and whole sectors are stored.
 template <bool BF16, int D>
 __global__ void __launch_bounds__(256, 4) k_kv_read(const KvView c, uint4 *k_out, uint4 *v_out, int64_t tokens)
 {
-    constexpr int kPieces = D / 16, kSteps = kHeads * kWindow * kPieces / 256;
+    constexpr int kPieces = D / 8, kSteps = kHeads * kWindow * kPieces / 256;
     __shared__ Places s;
     const int64_t t0 = (int64_t)blockIdx.x * kWindow;
     griddep_wait();
     griddep_release();
     find_places(c, t0, kWindow, tokens, s);
+    // Which piece of which token of each 256 / kPieces is the same in all steps.
+    constexpr int kTokens = 256 / kPieces; // a step's (token, head) pairs
+    const int x = threadIdx.x % kPieces, pair = threadIdx.x / kPieces;
     for (int h0 = blockIdx.y * kHeads; h0 < c.heads; h0 += gridDim.y * kHeads) {
-        uint4 v[kSteps][2];
-        float f[kSteps][2];
 #pragma unroll
-        for (int i = 0; i < kSteps; ++i) {
-            const int e = threadIdx.x + i * 256, x = e % kPieces, r = e / kPieces % kWindow;
-            const int h = h0 + e / (kPieces * kWindow);
-            if (s.page[r] >= 0 && h < c.heads) {
-                const int64_t block = (int64_t)s.page[r] * c.heads + h;
-                const int64_t at = (block * c.page_size + s.slot[r]) * kPieces + x;
-                v[i][0] = __ldg(reinterpret_cast<const uint4 *>(c.k) + at);
-                v[i][1] = __ldg(reinterpret_cast<const uint4 *>(c.v) + at);
-                f[i][0] = __ldg(c.ka + block);
-                f[i][1] = __ldg(c.va + block);
+        for (int kv = 0; kv < 2; ++kv) {
+            const uint2 *codes = reinterpret_cast<const uint2 *>(kv ? c.v : c.k);
+            const float *absmax = kv ? c.va : c.ka;
+            uint4 *out = kv ? v_out : k_out;
+            uint2 v[kSteps];
+            float f[kSteps];
+#pragma unroll
+            for (int i = 0; i < kSteps; ++i) {
+                const int e = pair + i * kTokens, r = e % kWindow, h = h0 + e / kWindow;
+                if (s.page[r] >= 0 && h < c.heads) {
+                    const int block = s.page[r] * c.heads + h; // fits: pages * heads * page_size < 2^31
+                    v[i] = __ldg(codes + ((int64_t)(block * c.page_size + s.slot[r])) * kPieces + x);
+                    f[i] = __ldg(absmax + block);
+                }
             }
-        }
 #pragma unroll
-        for (int i = 0; i < kSteps; ++i) {
-            const int e = threadIdx.x + i * 256, x = e % kPieces, r = e / kPieces % kWindow;
-            const int h = h0 + e / (kPieces * kWindow);
-            if (s.page[r] >= 0 && h < c.heads) {
-                const int64_t at = (((t0 + r) * c.heads + h) * kPieces + x) * 2;
-#pragma unroll
-                for (int kv = 0; kv < 2; ++kv) {
-                    uint4 *out = (kv ? v_out : k_out) + at;
-                    const float m = __fdiv_rn(f[i][kv], 127.0f);
-                    const int8_t *a = reinterpret_cast<const int8_t *>(&v[i][kv]);
-                    uint32_t o[8];
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        o[j] = down2<BF16>((float)a[2 * j] * m, (float)a[2 * j + 1] * m);
-                    out[0] = make_uint4(o[0], o[1], o[2], o[3]);
-                    out[1] = make_uint4(o[4], o[5], o[6], o[7]);
+            for (int i = 0; i < kSteps; ++i) {
+                const int e = pair + i * kTokens, r = e % kWindow, h = h0 + e / kWindow;
+                if (s.page[r] >= 0 && h < c.heads) {
+                    const float m = __fdiv_rn(f[i], 127.0f);
+                    const uint2 a = code_values4<BF16>(v[i].x, m), b = code_values4<BF16>(v[i].y, m);
+                    out[((t0 + r) * c.heads + h) * kPieces + x] = make_uint4(a.x, a.y, b.x, b.y);
                 }
             }
         }

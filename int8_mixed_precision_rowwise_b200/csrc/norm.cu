@@ -476,24 +476,42 @@ __global__ void __launch_bounds__(kMaxRowThreads, 1) k_norm_quant_wide(const Nor
     }
 }
 
-// value = code * (absmax / 127), 16 codes a thread.
+// value = code * (absmax / 127). A thread takes four vectors of 8 codes, a CTA's
+// width apart: 8-byte loads, all under way at once, and whole sectors stored. A
+// vector's row is carried along, not divided for.
 template <bool BF16>
-__global__ void __launch_bounds__(256) k_dequant_rows(const uint4 *__restrict__ codes,
-                                                      const float *__restrict__ absmax, int64_t n16, int row16,
+__global__ void __launch_bounds__(256) k_dequant_rows(const uint2 *__restrict__ codes,
+                                                      const float *__restrict__ absmax, int64_t n8, int row8,
                                                       uint4 *__restrict__ out)
 {
     griddep_wait();
     griddep_release();
-    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n16; i += (int64_t)gridDim.x * blockDim.x) {
-        const uint4 c = codes[i];
-        const float s = __fdiv_rn(absmax[i / row16], 127.0f);
-        const int8_t *b = reinterpret_cast<const int8_t *>(&c);
-        uint32_t o[8];
+    const int dr = 256 / row8, dc = 256 - dr * row8;
+    for (int64_t i0 = (int64_t)blockIdx.x * 1024 + threadIdx.x; i0 < n8; i0 += (int64_t)gridDim.x * 1024) {
+        int64_t row = n8 < ((int64_t)1 << 32) ? (int64_t)((uint32_t)i0 / (uint32_t)row8) : i0 / row8;
+        int col = (int)(i0 - row * row8);
+        uint2 c[4];
+        float s[4];
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            o[j] = down2<BF16>((float)b[2 * j] * s, (float)b[2 * j + 1] * s);
-        out[2 * i] = make_uint4(o[0], o[1], o[2], o[3]);
-        out[2 * i + 1] = make_uint4(o[4], o[5], o[6], o[7]);
+        for (int k = 0; k < 4; ++k) {
+            if (i0 + k * 256 < n8) {
+                c[k] = __ldcs(codes + i0 + k * 256);
+                s[k] = __ldg(absmax + row);
+            }
+            row += dr;
+            col += dc;
+            if (col >= row8) {
+                col -= row8;
+                ++row;
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (i0 + k * 256 < n8) {
+                const float m = __fdiv_rn(s[k], 127.0f);
+                const uint2 a = code_values4<BF16>(c[k].x, m), b = code_values4<BF16>(c[k].y, m);
+                out[i0 + k * 256] = make_uint4(a.x, a.y, b.x, b.y);
+            }
     }
 }
 
@@ -555,11 +573,10 @@ cudaError_t launch_norm_quant(const NormArgs &a, const Workspace &ws, const Devi
 cudaError_t launch_dequant_rows(const int8_t *codes, const float *absmax, int64_t rows, int64_t cols, void *out,
                                 bool bf16, const DeviceInfo &dev, cudaStream_t stream)
 {
-    const int64_t n16 = rows * cols / 16;
-    const int64_t grid = std::min<int64_t>((n16 + 255) / 256, (int64_t)dev.num_sms * 16);
+    const int64_t n8 = rows * cols / 8;
+    const int64_t grid = std::min<int64_t>((n8 + 1023) / 1024, (int64_t)dev.num_sms * 32);
     return launch_pdl(bf16 ? k_dequant_rows<true> : k_dequant_rows<false>, dim3((unsigned)grid), 256, 0, stream,
-                      reinterpret_cast<const uint4 *>(codes), absmax, n16, (int)(cols / 16),
-                      static_cast<uint4 *>(out));
+                      reinterpret_cast<const uint2 *>(codes), absmax, n8, (int)(cols / 8), static_cast<uint4 *>(out));
 }
 
 } // namespace llmint8
