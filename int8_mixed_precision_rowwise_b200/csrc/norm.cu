@@ -296,6 +296,13 @@ __global__ void __launch_bounds__(MAXT, 1024 / MAXT) k_norm_quant(const NormPara
             for (int i = 0; i < kVec; ++i)
                 v[i] = add8<BF16>(v[i], u[i]);
         }
+        // The CTA's next row on its way to L2 while this one is worked on.
+        if (r + gridDim.x < p.rows)
+            for (int line = tid * 8; line < nvec; line += blockDim.x * 8) {
+                asm volatile("prefetch.global.L2 [%0];" ::"l"(xr + (int64_t)gridDim.x * nvec + line));
+                if (p.res)
+                    asm volatile("prefetch.global.L2 [%0];" ::"l"(p.res + (r + gridDim.x) * nvec + line));
+            }
         // Most columns are found by the first rows: look often then, and later
         // now and again.
         if (THR && n > 0 && (n < 4 || (n & 7) == 0)) {
