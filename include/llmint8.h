@@ -556,8 +556,9 @@ LLMINT8_API size_t llmint8_kv_attention_workspace_size(int64_t heads, int64_t kv
  *   out          (device) [tokens x heads x head_dim] of `type`, dense
  *   lse          (device, may be NULL) fp32 [tokens x heads]
  *   workspace    (device) >= llmint8_kv_attention_workspace_size bytes, zeroed once
- * Errors: heads not a multiple of cache->heads is LLMINT8_ERR_UNSUPPORTED_SHAPE,
- * a scale that is not finite LLMINT8_ERR_INVALID_ARG; the others as
+ * out must not overlap Q or the cache. Errors: heads not a multiple of
+ * cache->heads, or more than 2^31 rows (tokens * heads / cache->heads), is
+ * LLMINT8_ERR_UNSUPPORTED_SHAPE, a scale that is not finite LLMINT8_ERR_INVALID_ARG; the others as
  * llmint8_kv_append. tokens == 0 or batch == 0 does nothing.
  */
 LLMINT8_API llmint8_status llmint8_kv_attention(const llmint8_kv_cache *cache, const void *Q, int type,

@@ -204,7 +204,8 @@ def get_workspace(nbytes: int, device):
 
 def workspaces(device=None) -> list:
     """The cached workspaces (of one device index, or all)."""
-    return [ws for (idx, _), ws in _workspaces.items() if device is None or idx == device]
+    return [ws for cached in (_workspaces, _serving_workspaces) for (idx, _), ws in cached.items()
+            if device is None or idx == device]
 
 
 def workspace_init(ws) -> None:
@@ -635,13 +636,36 @@ def _raw_stream(index):
     return get(index) if get else torch.cuda.current_stream(index).cuda_stream
 
 
-def _workspace(workspace, nbytes, index):
+# The workspaces of these calls, one per (device index, raw stream handle), of one
+# size that is enough for every shape: they never grow, so that a captured graph
+# never holds one that has been replaced. (get_workspace's, which the linears use,
+# grow.)
+_serving_workspaces: dict = {}
+
+
+def _workspace(workspace, index):
     """(address, bytes) of the given workspace, or of the one of the device's current stream."""
     if workspace is None:
-        workspace = _workspaces.get((index, _raw_stream(index)))
-        if workspace is None or workspace.numel() < nbytes:
-            workspace = get_workspace(nbytes, _torch().device("cuda", index))
+        workspace = _serving_workspaces.get((index, _raw_stream(index)))
+        if workspace is None:
+            workspace = _new_serving_workspace(index)
     return workspace.data_ptr(), workspace.numel()
+
+
+def _new_serving_workspace(index):
+    torch = _torch()
+    dev = torch.device("cuda", index)
+    nbytes = max(kv_attention_workspace_size(1, 1, 128), quantize_workspace_size(0, 133136))
+    with torch.cuda.device(index):
+        if torch.cuda.is_current_stream_capturing():
+            # What is captured is not executed yet: this workspace is the graph's own,
+            # and each replay clears the part whose state calls hand on.
+            ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+            ws[:quantize_workspace_size(0, 0)].zero_()
+            return ws
+        ws = torch.zeros(nbytes, dtype=torch.uint8, device=dev)
+        _serving_workspaces[(index, _raw_stream(index))] = ws
+        return ws
 
 
 def _call(where, index, *args):
@@ -654,9 +678,6 @@ def _call(where, index, *args):
             st = load()[where](*args, _raw_stream(index))
     if st:
         _check(st, "llmint8" + where)
-
-
-_quantize_workspace_size = functools.lru_cache(maxsize=256)(quantize_workspace_size)
 
 
 def add_rmsnorm_quantize(X, weight, residual=None, eps: float = 1e-6, threshold: float = 0.0, codes=None,
@@ -702,7 +723,7 @@ def add_rmsnorm_quantize(X, weight, residual=None, eps: float = 1e-6, threshold:
         residual_out = torch.empty_like(X)
     _call("_add_rmsnorm_quantize", index, X.data_ptr(), _ptr(residual), weight.data_ptr(), kind, rows, cols, eps,
           threshold, _ptr(residual_out), _ptr(Y), codes.data_ptr(), row_absmax.data_ptr(), _ptr(outlier_bitmap),
-          *_workspace(workspace, _quantize_workspace_size(rows, cols), index))
+          *_workspace(workspace, index))
     return codes, row_absmax, outlier_bitmap, Y, (X if residual_out is None else residual_out)
 
 
@@ -727,46 +748,66 @@ def dequantize_rowwise(codes, row_absmax, dtype=None, out=None):
 def _kv_cache(k_codes, v_codes, k_absmax, v_absmax, page_table, seq_lens, cu_rows):
     """(llmint8_kv_cache descriptor of checked tensors, device number)."""
     torch = _torch()
+    int8, int32, float32 = torch.int8, torch.int32, torch.float32
+    try:
+        index, shape = k_codes.get_device(), k_codes.shape
+        pages, heads, page_size, head_dim = shape
+        batch, width = page_table.shape
+        stride, step = page_table.stride()
+        per_page = (pages, heads)
+        fine = (index >= 0 and k_codes.dtype is int8 and k_codes.is_contiguous()
+                and v_codes.dtype is int8 and v_codes.shape == shape and v_codes.get_device() == index
+                and v_codes.is_contiguous()
+                and k_absmax.dtype is float32 and k_absmax.shape == per_page and k_absmax.get_device() == index
+                and k_absmax.is_contiguous()
+                and v_absmax.dtype is float32 and v_absmax.shape == per_page and v_absmax.get_device() == index
+                and v_absmax.is_contiguous()
+                and page_table.dtype is int32 and page_table.get_device() == index and (step == 1 or width < 2)
+                and (stride >= width or batch < 2)
+                and seq_lens.dtype is int32 and seq_lens.shape == (batch,) and seq_lens.get_device() == index
+                and seq_lens.is_contiguous()
+                and cu_rows.dtype is int32 and cu_rows.shape == (batch + 1,) and cu_rows.get_device() == index
+                and cu_rows.is_contiguous())
+    except (AttributeError, ValueError):
+        fine = False
+    if not fine:
+        _refuse_cache(k_codes, v_codes, k_absmax, v_absmax, page_table, seq_lens, cu_rows)
+    return _KvCache(k_codes.data_ptr(), v_codes.data_ptr(), k_absmax.data_ptr(), v_absmax.data_ptr(), pages, heads,
+                    page_size, head_dim, batch, width, stride if batch > 1 else width, page_table.data_ptr(),
+                    seq_lens.data_ptr(), cu_rows.data_ptr()), index
+
+
+def _refuse_cache(k_codes, v_codes, k_absmax, v_absmax, page_table, seq_lens, cu_rows):
+    """The reason why _kv_cache does not take these tensors."""
+    torch = _torch()
     index = _index(k_codes, "k_codes")
     if k_codes.dim() != 4 or k_codes.dtype is not torch.int8 or not k_codes.is_contiguous():
         raise ValueError("k_codes must be int8 [pages x heads x page_size x head_dim] and contiguous")
-    shape = k_codes.shape
-    pages, heads, page_size, head_dim = shape
-    _need_like(v_codes, "v_codes", torch.int8, shape, index)
+    pages, heads = k_codes.shape[:2]
+    _need_like(v_codes, "v_codes", torch.int8, k_codes.shape, index)
     _need_like(k_absmax, "k_absmax", torch.float32, (pages, heads), index)
     _need_like(v_absmax, "v_absmax", torch.float32, (pages, heads), index)
     _index(page_table, "page_table")
     if page_table.dim() != 2 or page_table.dtype is not torch.int32 or page_table.get_device() != index:
         raise ValueError(f"page_table must be int32 [batch x pages of a sequence] on cuda:{index}")
-    batch, width = page_table.shape
-    stride, step = page_table.stride()
-    if batch < 2:
-        stride = width
-    if (width > 1 and step != 1) or stride < width:
-        raise ValueError("page_table's rows must be contiguous and apart")
+    batch = page_table.shape[0]
     _need_like(seq_lens, "seq_lens", torch.int32, (batch,), index)
     _need_like(cu_rows, "cu_rows", torch.int32, (batch + 1,), index)
-    return _KvCache(k_codes.data_ptr(), v_codes.data_ptr(), k_absmax.data_ptr(), v_absmax.data_ptr(), pages, heads,
-                    page_size, head_dim, batch, width, stride, page_table.data_ptr(), seq_lens.data_ptr(),
-                    cu_rows.data_ptr()), index
+    raise ValueError("page_table's rows must be contiguous and apart")
 
 
-def _need_rows(t, name, heads, head_dim, index):
-    """Packed rows [tokens x heads x head_dim], fp16 or bf16, the last dimension dense."""
+def _rows(t, name, heads, head_dim, index):
+    """(type, token stride, head stride) of packed rows [tokens x heads x head_dim], fp16 or bf16, the last
+    dimension dense. A dimension of one is never stepped: its stride is 0."""
     if _index(t, name) != index:
         raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
     kind = _value_type(t, name)
     if t.dim() != 3 or t.shape[2] != head_dim or (heads is not None and t.shape[1] != heads):
         raise ValueError(f"{name} must be [tokens x {heads or 'heads'} x {head_dim}], got {list(t.shape)}")
-    if t.stride(2) != 1:
+    token, head, step = t.stride()
+    if step != 1:
         raise ValueError(f"{name}'s last dimension must be contiguous")
-    return kind
-
-
-def _row_strides(t):
-    """Strides between tokens and between heads (0 where there is only one: it is never stepped)."""
-    tok, head, _ = t.stride()
-    return tok if t.shape[0] > 1 else 0, head if t.shape[1] > 1 else 0
+    return kind, token if t.shape[0] > 1 else 0, head if t.shape[1] > 1 else 0
 
 
 def kv_append(K, V, k_codes, v_codes, k_absmax, v_absmax, page_table, seq_lens, cu_rows, workspace=None):
@@ -776,11 +817,13 @@ def kv_append(K, V, k_codes, v_codes, k_absmax, v_absmax, page_table, seq_lens, 
     are the last positions of sequence b, whose length with them is seq_lens[b] and whose pages are
     page_table[b] (llmint8_kv_append)."""
     c, index = _kv_cache(k_codes, v_codes, k_absmax, v_absmax, page_table, seq_lens, cu_rows)
-    kind = _need_rows(K, "K", c.heads, c.head_dim, index)
-    if _need_rows(V, "V", c.heads, c.head_dim, index) != kind or V.shape != K.shape:
+    kind, k_token, k_head = _rows(K, "K", c.heads, c.head_dim, index)
+    v_kind, v_token, v_head = _rows(V, "V", c.heads, c.head_dim, index)
+    tokens = K.shape[0]
+    if v_kind != kind or V.shape[0] != tokens:
         raise ValueError("K and V must have the same type and shape")
-    _call("_kv_append", index, ctypes.byref(c), K.data_ptr(), V.data_ptr(), kind, K.shape[0], *_row_strides(K),
-          *_row_strides(V), *_workspace(workspace, 4096, index))
+    _call("_kv_append", index, ctypes.byref(c), K.data_ptr(), V.data_ptr(), kind, tokens, k_token, k_head, v_token,
+          v_head, *_workspace(workspace, index))
 
 
 def kv_read(k_codes, v_codes, k_absmax, v_absmax, page_table, seq_lens, cu_rows, tokens: int, dtype=None, K=None,
@@ -800,15 +843,12 @@ def kv_read(k_codes, v_codes, k_absmax, v_absmax, page_table, seq_lens, cu_rows,
     else:
         _need_like(V, "V", dtype, shape, index)
     _call("_kv_read", index, ctypes.byref(c), K.data_ptr(), V.data_ptr(), _value_type(K, "K"), shape[0],
-          *_workspace(workspace, 4096, index))
+          *_workspace(workspace, index))
     return K, V
 
 
 def kv_attention_workspace_size(heads: int, kv_heads: int, head_dim: int) -> int:
     return int(load()["_kv_attention_workspace_size"](heads, kv_heads, head_dim))
-
-
-_attention_workspace_size = functools.lru_cache(maxsize=256)(kv_attention_workspace_size)
 
 
 def kv_attention(Q, k_codes, v_codes, k_absmax, v_absmax, page_table, seq_lens, cu_rows, scale: float | None = None,
@@ -822,7 +862,7 @@ def kv_attention(Q, k_codes, v_codes, k_absmax, v_absmax, page_table, seq_lens, 
     torch = _torch()
     c, index = _kv_cache(k_codes, v_codes, k_absmax, v_absmax, page_table, seq_lens, cu_rows)
     head_dim = c.head_dim
-    kind = _need_rows(Q, "Q", None, head_dim, index)
+    kind, q_token, q_head = _rows(Q, "Q", None, head_dim, index)
     tokens, heads, _ = shape = Q.shape
     if alibi_slopes is not None:
         _need_like(alibi_slopes, "alibi_slopes", torch.float32, (heads,), index)
@@ -834,9 +874,9 @@ def kv_attention(Q, k_codes, v_codes, k_absmax, v_absmax, page_table, seq_lens, 
         _need_like(lse, "lse", torch.float32, (tokens, heads), index)
     if scale is None:
         scale = head_dim ** -0.5
-    _call("_kv_attention", index, ctypes.byref(c), Q.data_ptr(), kind, tokens, heads, *_row_strides(Q), scale,
+    _call("_kv_attention", index, ctypes.byref(c), Q.data_ptr(), kind, tokens, heads, q_token, q_head, scale,
           1 if causal else 0, _ptr(alibi_slopes), max_new, out.data_ptr(), _ptr(lse),
-          *_workspace(workspace, _attention_workspace_size(heads, c.heads, head_dim), index))
+          *_workspace(workspace, index))
     return out
 
 

@@ -596,7 +596,7 @@ llmint8_status llmint8_kv_attention(const llmint8_kv_cache *cache, const void *Q
         return st;
     if (!value_type(type) || (tokens > 0 && (!Q || !out)) || heads <= 0 || max_new < 0 || std::isnan(scale) || std::isinf(scale))
         return LLMINT8_ERR_INVALID_ARG;
-    if (heads % cache->heads != 0 || heads > 65535)
+    if (heads % cache->heads != 0 || heads > 65535 || tokens * (heads / cache->heads) > INT32_MAX)
         return LLMINT8_ERR_UNSUPPORTED_SHAPE;
     if (!aligned16(Q) || !aligned16(out) || !row_stride(q_token_stride) || !row_stride(q_head_stride) ||
         (reinterpret_cast<uintptr_t>(alibi_slopes) & 3u) || (reinterpret_cast<uintptr_t>(lse) & 3u))

@@ -348,6 +348,59 @@ def test_decode_steps_captured_and_replayed(lib):
     assert lib.read_status(ws) == 0
 
 
+def test_first_use_inside_a_capture(lib):
+    """Graphs that are captured on streams where these calls were never made before: each replay starts from a clean
+    workspace of its own, whatever the memory held; eager calls in between are not disturbed."""
+    g = torch.Generator().manual_seed(17)
+    lens = [700, 333]
+    table, pages = page_table(lens, 16, g, "cuda")
+    bufs = random_cache(pages, 2, 16, 128, g, "cuda")
+    Q = rows((2, 8, 128), g, F16)
+    n, at = ints(lens), ints([0, 1, 2])
+    ref, _, tol = attention_reference(Q, *bufs, table, lens, [1, 1], 128 ** -0.5)
+    x = rows((3, 512), g, F16)
+    w = torch.ones(512, dtype=F16, device="cuda")
+    dirt = torch.full((64 << 20,), 255, dtype=torch.uint8, device="cuda")
+    del dirt  # what the allocator hands out next is not zeros
+    graphs = []
+    for _ in range(2):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=torch.cuda.Stream()):
+            a = lib.kv_attention(Q, *bufs, table, n, at)
+            b = lib.add_rmsnorm_quantize(x, w, threshold=1.5)
+        graphs.append((graph, a, b))
+    want = lib.add_rmsnorm_quantize(x, w, threshold=1.5)
+    for _ in range(3):
+        for graph, a, b in graphs:
+            a.zero_()
+            graph.replay()
+            torch.cuda.synchronize()
+            check_attention(a, ref, tol, F16)
+            assert all(torch.equal(p, q) for p, q in zip(b[:4], want[:4]))
+            check_attention(lib.kv_attention(Q, *bufs, table, n, at), ref, tol, F16)
+
+
+def test_calls_on_two_streams_at_once(lib):
+    """The same calls on two streams, each with a workspace of its own, give what one after the other does."""
+    g = torch.Generator().manual_seed(18)
+    lens = [2000, 1500, 900]
+    table, pages = page_table(lens, 32, g, "cuda")
+    bufs = random_cache(pages, 4, 32, 128, g, "cuda")
+    n = ints(lens)
+    cases = [(rows((3, 16, 128), g, F16), ints([0, 1, 2, 3])), (rows((600, 16, 128), g, F16), ints([0, 250, 500, 600]))]
+    want = [lib.kv_attention(q, *bufs, table, n, at) for q, at in cases]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    got = [[] for _ in cases]
+    for _ in range(5):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(lib.kv_attention(*(cases[i][0],), *bufs, table, n, cases[i][1]))
+    torch.cuda.synchronize()
+    for i, outs in enumerate(got):
+        assert all(torch.equal(o, want[i]) for o in outs)
+
+
 def test_a_block_of_operators_together(lib):
     """A prompt and two decode steps through one attention block as it would be served: norm and quantization, the
     int8 qkv linear, the cache, attention, the int8 output linear. Each stage against its definition on the inputs

@@ -110,7 +110,7 @@ def test_row_argument_errors(lib):
     for bad in (dict(Q=None), dict(out=None), dict(heads=0), dict(heads=-2), dict(scale=float("nan")),
                 dict(scale=float("inf")), dict(max_new=-1)):
         assert attend(good, **bad) == lib.ERR_INVALID_ARG, bad
-    for bad in (dict(heads=3), dict(heads=65538)):
+    for bad in (dict(heads=3), dict(heads=65538), dict(heads=8, tokens=1 << 29)):
         assert attend(good, **bad) == lib.ERR_UNSUPPORTED_SHAPE, bad
     for bad in (dict(Q=A + 2), dict(out=A + 8), dict(s=(256, 4)), dict(s=(-256, 64)), dict(slopes=A + 2),
                 dict(lse=A + 2)):
