@@ -321,8 +321,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_prefill(const __grid_const
                 const bool each = ALIBI || key + kUnit - 1 > lim_min;
                 // The maximum so far mostly will do: that none of the weights
                 // is too large shows in their sum. If one is, the scores (still
-                // in tensor memory) are read again and the maximum moves.
-                bool move = first;
+                // in tensor memory) are read again and the maximum moves. A row
+                // that has not met a key yet has none.
+                bool move = first || __any_sync(0xffffffffu, m == -INFINITY);
                 uint32_t w16[64];
                 float sum_l;
                 for (;;) {

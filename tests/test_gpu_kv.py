@@ -158,6 +158,38 @@ def test_pages_outside_the_cache_are_left_out(lib):
     assert bool(((lse - ref_lse).abs() <= 1e-4).all())
 
 
+@pytest.mark.parametrize("news,heads,kv_heads", [(1, 4, 1), (40, 4, 1), (1, 112, 112), (40, 112, 112)])
+def test_the_first_keys_missing_and_the_others_far_below(lib, news, heads, kv_heads):
+    """The first 160 positions without pages, and scores of the others near -600: the rows' maximum is far below zero
+    when it is first known, in a unit of keys that is not the first (with 112 heads, of one CTA's)."""
+    g = torch.Generator().manual_seed(4)
+    lens = [500]
+    table, pages = page_table(lens, 16, g, "cuda")
+    k, v, ka, va = random_cache(pages, kv_heads, 16, 128, g, "cuda")
+    table[0, :10] = -1
+    k.copy_(torch.randint(100, 128, k.shape, generator=g, dtype=torch.int8))
+    ka.fill_(1.0)
+    Q = (-60 - rows((news, heads, 128), g, F16).abs())
+    ws = torch.zeros(lib.kv_attention_workspace_size(heads, kv_heads, 128), dtype=torch.uint8, device="cuda")
+    ref, _, tol = attention_reference(Q, k, v, ka, va, table, lens, [news], 128 ** -0.5)
+    out = lib.kv_attention(Q, k, v, ka, va, table, ints(lens), ints([0, news]), workspace=ws)
+    assert lib.read_status(ws) == 0x20
+    assert ref.abs().max() > 0.1
+    check_attention(out, ref, tol, F16)
+
+
+@pytest.mark.parametrize("news", [1, 40])
+@pytest.mark.parametrize("scale", [-0.2, 0.0, 3.0])
+def test_attention_scales(lib, news, scale):
+    g = torch.Generator().manual_seed(5)
+    table, pages = page_table([300], 32, g, "cuda")
+    bufs = random_cache(pages, 2, 32, 64, g, "cuda")
+    for dtype in (F16, BF16):
+        Q = rows((news, 4, 64), g, dtype)
+        ref, _, tol = attention_reference(Q, *bufs, table, [300], [news], scale)
+        check_attention(lib.kv_attention(Q, *bufs, table, ints([300]), ints([0, news]), scale=scale), ref, tol, dtype)
+
+
 def run_attention(lib, page, dim, heads, kv_heads, dtype, lens, news, causal=True, alibi=False, seed=0, q_scale=1.0,
                   max_new=None, extra_rows=1, cache=None, **more):
     g = torch.Generator().manual_seed(seed)

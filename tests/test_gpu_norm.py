@@ -82,6 +82,13 @@ def test_norm_without_residual_and_without_y(lib, oracle_mod):
     assert not bitmap.any()  # no threshold: the bitmap is cleared
 
 
+def test_norm_of_no_rows(lib):
+    x = torch.empty((0, 64), dtype=torch.float16, device="cuda")
+    codes, absmax, bitmap, Y, h = lib.add_rmsnorm_quantize(x, torch.ones(64, dtype=torch.float16, device="cuda"), x,
+                                                           threshold=6.0)
+    assert codes.shape == Y.shape == h.shape == (0, 64) and absmax.shape == (0,) and not bitmap.any()
+
+
 @pytest.mark.parametrize("cols", [1024, 40000])
 @pytest.mark.parametrize("into", ["X", "residual"])
 def test_norm_in_place(lib, oracle_mod, cols, into):
