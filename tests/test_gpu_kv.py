@@ -178,6 +178,27 @@ def test_the_first_keys_missing_and_the_others_far_below(lib, news, heads, kv_he
     check_attention(out, ref, tol, F16)
 
 
+@pytest.mark.parametrize("news", [1, 12, 40, 300])
+@pytest.mark.parametrize("dim,dtype,alibi", [(128, F16, False), (64, BF16, False), (128, BF16, True)])
+def test_scores_that_grow_along_the_sequence(lib, news, dim, dtype, alibi):
+    """Enough heads and keys that a CTA runs through several units of an item, with scores that grow from page to
+    page, by little, by much and by leaps: the running maximum moves in the middle of it, for some rows."""
+    g = torch.Generator().manual_seed(news + dim)
+    lens, kv_heads = [1500, 1400, 1450], 40
+    table, pages = page_table(lens, 32, g, "cuda")
+    k, v, ka, va = random_cache(pages, kv_heads, 32, dim, g, "cuda")
+    for b in range(3):
+        for j in range(lens[b] // 32):
+            ka[table[b, j].long()] *= (1 + j / 10) if b == 0 else 1.3 ** j * 1e-3 if b == 1 else (40.0 if j % 11 == 10 else 0.1)
+    Q = rows((3 * news, kv_heads, dim), g, dtype, 2.0)
+    slopes = torch.linspace(0.001, 2.0, kv_heads, device="cuda") if alibi else None
+    ref, ref_lse, tol = attention_reference(Q, k, v, ka, va, table, lens, [news] * 3, dim ** -0.5, slopes=slopes)
+    lse = torch.empty((3 * news, kv_heads), device="cuda")
+    out = lib.kv_attention(Q, k, v, ka, va, table, ints(lens), cu([news] * 3, "cuda"), alibi_slopes=slopes, lse=lse)
+    check_attention(out, ref, tol, dtype)
+    assert bool(((lse - ref_lse).abs() <= 2.0 ** -10 + 2.0 ** -17 * ref_lse.abs()).all())
+
+
 @pytest.mark.parametrize("news", [1, 40])
 @pytest.mark.parametrize("scale", [-0.2, 0.0, 3.0])
 def test_attention_scales(lib, news, scale):
