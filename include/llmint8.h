@@ -534,6 +534,12 @@ LLMINT8_API llmint8_status llmint8_kv_append(const llmint8_kv_cache *cache, cons
 LLMINT8_API llmint8_status llmint8_kv_read(const llmint8_kv_cache *cache, void *K, void *V, int type, int64_t tokens,
                                void *workspace, size_t ws_bytes, llmint8_stream_t stream);
 
+/* The number of the capture into a CUDA graph that the stream takes part in
+ * (no other capture of the process has it), 0 outside of one. What a graph's
+ * calls hand on in a workspace must not be shared with calls that may run
+ * while the graph is replayed: with this a caller finds each capture its own. */
+LLMINT8_API uint64_t llmint8_stream_capture_id(llmint8_stream_t stream);
+
 /* Bytes of workspace needed by llmint8_kv_attention. */
 LLMINT8_API size_t llmint8_kv_attention_workspace_size(int64_t heads, int64_t kv_heads, int64_t head_dim);
 

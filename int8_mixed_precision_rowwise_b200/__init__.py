@@ -87,6 +87,7 @@ _SIGNATURES = {
     "llmint8_kv_append": (_ST, [ctypes.POINTER(_KvCache), _P, _P, ctypes.c_int, _I64, _I64, _I64, _I64, _I64, _P,
                                 ctypes.c_size_t, _P]),
     "llmint8_kv_read": (_ST, [ctypes.POINTER(_KvCache), _P, _P, ctypes.c_int, _I64, _P, ctypes.c_size_t, _P]),
+    "llmint8_stream_capture_id": (ctypes.c_uint64, [_P]),
     "llmint8_kv_attention_workspace_size": (ctypes.c_size_t, [_I64, _I64, _I64]),
     "llmint8_kv_attention": (_ST, [ctypes.POINTER(_KvCache), _P, ctypes.c_int, _I64, _I64, _I64, _I64, ctypes.c_float,
                                    ctypes.c_int, _P, _I64, _P, _P, _P, ctypes.c_size_t, _P]),
@@ -203,7 +204,8 @@ def get_workspace(nbytes: int, device):
 
 
 def workspaces(device=None) -> list:
-    """The cached workspaces (of one device index, or all)."""
+    """The cached workspaces (of one device index, or all). Those that belong to captured graphs are not
+    among them (to read the status of replays, give the captured calls a workspace)."""
     return [ws for cached in (_workspaces, _serving_workspaces) for (idx, _), ws in cached.items()
             if device is None or idx == device]
 
@@ -637,35 +639,46 @@ def _raw_stream(index):
 
 
 # The workspaces of these calls, one per (device index, raw stream handle), of one
-# size that is enough for every shape: they never grow, so that a captured graph
-# never holds one that has been replaced. (get_workspace's, which the linears use,
-# grow.)
+# size that is enough for every shape, so that they never grow. (get_workspace's,
+# which the linears use, do.) Calls that are captured get one of the graph's own,
+# from its memory: a graph may be replayed on any stream, next to calls on the one it
+# was captured on and to other graphs captured there. Per stream the latest capture's
+# is remembered, with the number of that capture.
 _serving_workspaces: dict = {}
+_captured_workspaces: dict = {}
 
 
 def _workspace(workspace, index):
     """(address, bytes) of the given workspace, or of the one of the device's current stream."""
     if workspace is None:
-        workspace = _serving_workspaces.get((index, _raw_stream(index)))
-        if workspace is None:
-            workspace = _new_serving_workspace(index)
+        stream = _raw_stream(index)
+        capture = load()["_stream_capture_id"](stream) if stream else 0  # the default stream is never captured
+        if capture:
+            held = _captured_workspaces.get((index, stream))
+            workspace = held[1] if held and held[0] == capture else _new_captured_workspace(index, stream, capture)
+        else:
+            workspace = _serving_workspaces.get((index, stream))
+            if workspace is None:
+                workspace = _serving_workspaces[(index, stream)] = _new_serving_workspace(index, True)
     return workspace.data_ptr(), workspace.numel()
 
 
-def _new_serving_workspace(index):
+def _new_serving_workspace(index, cleared):
     torch = _torch()
-    dev = torch.device("cuda", index)
-    nbytes = max(kv_attention_workspace_size(1, 1, 128), quantize_workspace_size(0, 133136))
+    make = torch.zeros if cleared else torch.empty
+    return make(max(kv_attention_workspace_size(1, 1, 128), quantize_workspace_size(0, 133136)), dtype=torch.uint8,
+                device=torch.device("cuda", index))
+
+
+def _new_captured_workspace(index, stream, capture):
+    torch = _torch()
+    _captured_workspaces.pop((index, stream), None)  # its memory may serve again
     with torch.cuda.device(index):
-        if torch.cuda.is_current_stream_capturing():
-            # What is captured is not executed yet: this workspace is the graph's own,
-            # and each replay clears the part whose state calls hand on.
-            ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-            ws[:quantize_workspace_size(0, 0)].zero_()
-            return ws
-        ws = torch.zeros(nbytes, dtype=torch.uint8, device=dev)
-        _serving_workspaces[(index, _raw_stream(index))] = ws
-        return ws
+        ws = _new_serving_workspace(index, False)
+        # Captured like all else: every replay starts with the part cleared whose state calls hand on.
+        ws[:quantize_workspace_size(0, 0)].zero_()
+    _captured_workspaces[(index, stream)] = capture, ws
+    return ws
 
 
 def _call(where, index, *args):

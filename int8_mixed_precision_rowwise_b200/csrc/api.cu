@@ -579,6 +579,15 @@ llmint8_status llmint8_kv_read(const llmint8_kv_cache *cache, void *K, void *V, 
                                       static_cast<uint32_t *>(workspace), dev, stream));
 }
 
+uint64_t llmint8_stream_capture_id(llmint8_stream_t stream)
+{
+    cudaStreamCaptureStatus status = cudaStreamCaptureStatusNone;
+    unsigned long long id = 0;
+    if (cudaStreamGetCaptureInfo(stream, &status, &id) != cudaSuccess)
+        return 0;
+    return status == cudaStreamCaptureStatusActive ? id : 0;
+}
+
 size_t llmint8_kv_attention_workspace_size(int64_t heads, int64_t kv_heads, int64_t head_dim)
 {
     if (heads <= 0 || kv_heads <= 0 || head_dim <= 0)

@@ -34,11 +34,9 @@ cudaError_t launch_kv_attention(const llmint8_kv_cache &c, const AttnArgs &a, co
     // A sequence's rows (new tokens x heads of a group) decide: up to 16 go to
     // the kernel that streams the cache once for them, more to the one that
     // fills tensor core tiles of 256. The lengths are on the device, so a batch
-    // that may hold both kinds gets both launches, and each takes its own.
-    // (Without a bound, as many rows as sequences are taken for one each.) A
+    // that may hold both kinds gets both launches, and each takes its own. A
     // bound that is wrong costs time only: a kernel that is alone takes all.
-    const int64_t bound = a.max_new > 0 ? std::min(a.max_new, a.tokens) : a.tokens <= c.batch ? 1 : a.tokens;
-    const int64_t most = bound * p.group;
+    const int64_t most = std::min(a.max_new, a.tokens) * p.group;
     const bool few = most <= kAttnFewRows;
     if (few || c.batch > 1) {
         p.rows_from = 1;

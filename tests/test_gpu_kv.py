@@ -433,6 +433,46 @@ def test_first_use_inside_a_capture(lib):
             check_attention(lib.kv_attention(Q, *bufs, table, n, at), ref, tol, F16)
 
 
+def test_graphs_captured_on_a_used_stream_run_at_once(lib):
+    """Two graphs captured on a stream where these calls were made before have workspaces of their own, one each,
+    apart from the stream's: replayed on two streams at once, next to calls on the one they were captured on, all
+    give what each gives alone."""
+    g = torch.Generator().manual_seed(23)
+    lens = [5000, 3000, 900]
+    table, pages = page_table(lens, 16, g, "cuda")
+    bufs = random_cache(pages, 4, 16, 128, g, "cuda")
+    n, at = ints(lens), ints([0, 1, 2, 3])
+    q = [rows((3, 16, 128), g, F16) for _ in range(3)]
+    want = [lib.kv_attention(x, *bufs, table, n, at, max_new=1) for x in q]
+    out = [torch.zeros_like(x) for x in q]
+    torch.cuda.synchronize()
+    s, others = torch.cuda.Stream(), [torch.cuda.Stream(), torch.cuda.Stream()]
+    used, graphs = [], []
+    with torch.cuda.stream(s):
+        lib.kv_attention(q[2], *bufs, table, n, at, max_new=1, out=out[2])
+        used.append(lib._workspace(None, s.device_index)[0])
+        for i in range(2):
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph, stream=s):
+                for _ in range(3):
+                    lib.kv_attention(q[i], *bufs, table, n, at, max_new=1, out=out[i])
+                    used.append(lib._workspace(None, s.device_index)[0])
+            graphs.append(graph)
+    torch.cuda.synchronize()
+    assert used[1] == used[2] == used[3] and used[4] == used[5] == used[6] and len(set(used)) == 3
+    for _ in range(5):
+        for graph, o in zip(graphs, others):
+            with torch.cuda.stream(o):
+                graph.replay()
+        with torch.cuda.stream(s):
+            lib.kv_attention(q[2], *bufs, table, n, at, max_new=1, out=out[2])
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(out, want))
+        for x in out:
+            x.zero_()
+        torch.cuda.synchronize()
+
+
 def test_calls_on_two_streams_at_once(lib):
     """The same calls on two streams, each with a workspace of its own, give what one after the other does."""
     g = torch.Generator().manual_seed(18)
