@@ -228,7 +228,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_prefill(const __grid_const
     }
     griddep_wait();
     griddep_release();
-    const Range range = my_range<kThreads>(p, smem + L::RAW, s_start);
+    const Range range = my_range<kThreads>(p, smem + L::META, s_start);
     if (range.u0 >= range.u1)
         return;
     if (warp == 12) {
@@ -267,7 +267,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_prefill(const __grid_const
             if (key < 0 || *s_abort)
                 break;
             ++walked;
-            const bool active = sub < info->subs, first = info->first;
+            const bool active = sub < info->subs, first = info->first, last = info->last;
             if (active && first) {
                 // The row into swizzled shared memory. All products of the
                 // segment before are complete (its last scores were read).
@@ -428,7 +428,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_prefill(const __grid_const
                     mbar_arrive(bar(P_FULL + sub));
                 ++mine;
             }
-            if (!info->last) {
+            if (!last) {
+                __syncwarp(); // all lanes have read what the slot says
                 if (lane == 0)
                     mbar_arrive(bar(META_EMPTY + slot));
                 continue;
@@ -450,10 +451,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_prefill(const __grid_const
                 wait(bar(O_FULL + sub), (mine - 1) & 1);
                 __syncwarp();
                 tc_fence_after();
-                // Through the half's query area, free now, a warp its own rows:
-                // 256 bytes of each at a time, so that whole lines are written.
+                // Through the query area, free now, in its layout: each warp its
+                // own rows, as the next segment's queries may come into the
+                // others' already. 2 D bytes of a row at a time, so that whole
+                // lines are written.
                 const float inv = whole ? (l > 0.f ? 1.0f / l : 0.f) : 1.f;
-                uint8_t *stage = smem + L::Q + sub * NH * kHalf + (warp & 3) * (NH * kHalf / 4);
+                uint8_t *stage = smem + L::Q + sub * NH * kHalf + (warp & 3) * 32 * 128;
+                auto staged = [&](int row, int ch) {
+                    return reinterpret_cast<uint4 *>(stage + (ch / 8) * kHalf + row * 128 + (((ch & 7) ^ (row & 7)) << 4));
+                };
                 constexpr int kRowBytes = D * 2, kCh = kRowBytes / 16; // 16-byte pieces of a staged row
                 const uint64_t to = whole ? reinterpret_cast<uint64_t>(static_cast<uint16_t *>(p.out) + at * D)
                                           : reinterpret_cast<uint64_t>(part + row * D);
@@ -473,12 +479,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_prefill(const __grid_const
                             }
 #pragma unroll
                             for (int x = 0; x < 2; ++x)
-                                *reinterpret_cast<uint4 *>(stage + lane * kRowBytes + (((k / 8 + x) ^ (lane & 7)) << 4)) =
+                                *staged(lane, k / 8 + x) =
                                     make_uint4(v[4 * x], v[4 * x + 1], v[4 * x + 2], v[4 * x + 3]);
                         } else {
 #pragma unroll
                             for (int x = 0; x < 4; ++x)
-                                *reinterpret_cast<uint4 *>(stage + lane * kRowBytes + (((k / 4 + x) ^ (lane & 7)) << 4)) =
+                                *staged(lane, k / 4 + x) =
                                     make_uint4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
                         }
                     }
@@ -488,8 +494,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_prefill(const __grid_const
                         const int of = k * (32 / kCh) + lane / kCh, ch = lane % kCh;
                         const uint64_t dst = __shfl_sync(0xffffffffu, to, of);
                         if (__shfl_sync(0xffffffffu, (int)live, of))
-                            *reinterpret_cast<uint4 *>(dst + pass * kRowBytes + ch * 16) =
-                                *reinterpret_cast<const uint4 *>(stage + of * kRowBytes + ((ch ^ (of & 7)) << 4));
+                            *reinterpret_cast<uint4 *>(dst + pass * kRowBytes + ch * 16) = *staged(of, ch);
                     }
                     __syncwarp();
                 }
@@ -730,6 +735,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_prefill(const __grid_const
                 store_meta(s_meta + ((i % kMetaRing) * kGroups + group) * 4, u0, fabsf(p.scale_log2));
                 const bool load = loads && u0.page >= 0;
                 const uint32_t which = __ballot_sync(0xffffffffu, load);
+                __syncwarp(); // all lanes' scales are written
                 if (lane == 0)
                     mbar_arrive(bar(META_FULL + i % kMetaRing));
 #pragma unroll

@@ -246,6 +246,16 @@ def test_attention_of_single_tokens(lib, page, dim, heads, kv_heads, dtype):
 
 
 @pytest.mark.parametrize("dtype,dim", [(F16, 128), (BF16, 64)])
+def test_many_short_sequences_one_after_the_other_in_a_cta(lib, dtype, dim):
+    """Each CTA ends items and begins the next ones several times over, its warps at their own pace; twice the same."""
+    g = torch.Generator().manual_seed(29)
+    news = torch.randint(5, 40, (160,), generator=g).tolist()
+    lens = [n + e for n, e in zip(news, torch.randint(0, 90, (160,), generator=g).tolist())]
+    first, again = (run_attention(lib, 16, dim, 32, 4, dtype, lens, news, seed=31) for _ in range(2))
+    assert torch.equal(first, again)
+
+
+@pytest.mark.parametrize("dtype,dim", [(F16, 128), (BF16, 64)])
 @pytest.mark.parametrize("page,heads,kv_heads,alibi", [(16, 8, 2, False), (16, 5, 5, True), (32, 8, 1, True),
                                                        (64, 32, 2, False), (128, 3, 3, False)])
 @pytest.mark.parametrize("causal", [True, False])
