@@ -660,6 +660,8 @@ def _workspace(workspace, index):
             workspace = _serving_workspaces.get((index, stream))
             if workspace is None:
                 workspace = _serving_workspaces[(index, stream)] = _new_serving_workspace(index, True)
+    elif workspace.get_device() != index or workspace.dtype is not _torch().uint8 or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous uint8 tensor on cuda:{index}")
     return workspace.data_ptr(), workspace.numel()
 
 

@@ -134,3 +134,13 @@ def test_binding_refuses_cpu_tensors(lib):
         lib.kv_read(c, c, a, a, i, i[0, :1], i[0], 1)
     with pytest.raises(TypeError):
         lib.kv_attention(q, c, c, a, a, i, i[0, :1], i[0])
+
+
+def test_workspaces_that_do_not_fit_are_refused(lib):
+    for bad in (torch.zeros(4096, dtype=torch.uint8), torch.zeros(4096, dtype=torch.uint8, device="meta")):
+        with pytest.raises(ValueError):
+            lib._workspace(bad, 0)
+
+
+def test_streams_outside_of_captures_have_no_number(lib):
+    assert lib.load()["_stream_capture_id"](None) == 0
