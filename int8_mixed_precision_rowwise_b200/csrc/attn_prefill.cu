@@ -264,7 +264,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_prefill(const __grid_const
             __syncwarp();
             const volatile UnitInfo *info = s_info + slot;
             const int key = info->key;
-            if (key < 0 || *s_abort)
+            if (__any_sync(0xffffffffu, key < 0 || *s_abort)) // the whole warp or none of it
                 break;
             ++walked;
             const bool active = sub < info->subs, first = info->first, last = info->last;
@@ -568,7 +568,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_prefill(const __grid_const
         const int r = tid & 127; // a key each
         for (int i = 0;; ++i) {
             wait(bar(META_FULL + i % kMetaRing), (i / kMetaRing) & 1);
-            if (reinterpret_cast<const volatile UnitInfo *>(s_info)[i % kMetaRing].key < 0 || *s_abort)
+            const int key = reinterpret_cast<const volatile UnitInfo *>(s_info)[i % kMetaRing].key;
+            if (__any_sync(0xffffffffu, key < 0 || *s_abort))
                 break;
 #pragma unroll 1
             for (int kv = 0; kv < 2; ++kv) {
