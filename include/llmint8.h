@@ -440,7 +440,9 @@ LLMINT8_API llmint8_status llmint8_noalloc_read_status(int clear, uint32_t *out)
  *   h[i,c] = X[i,c] + residual[i,c], rounded to `type` (h = X without residual)
  *   y[i,c] = fp16( h[i,c] * weight[c] / sqrt(mean_c(h[i,:]^2) + eps) ), in fp32
  * and codes, row_absmax and outlier_bitmap are exactly what
- * llmint8_quantize_rowwise(y, threshold) gives.
+ * llmint8_quantize_rowwise(y, threshold) gives. Where Y is not asked for, the
+ * multiplier of the codes is 127 * (1 / absmax) in place of 127 / absmax, each
+ * step rounded to fp32: another code only where y lies between two of them.
  *   X            (device) [rows x cols]; cols a multiple of 16
  *   residual     (device, may be NULL) [rows x cols]
  *   weight       (device) [cols]

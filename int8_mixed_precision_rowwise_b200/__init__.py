@@ -701,7 +701,8 @@ def add_rmsnorm_quantize(X, weight, residual=None, eps: float = 1e-6, threshold:
     h = X + residual [rows x cols] (fp16 or bf16) and Y = h * weight / sqrt(mean(h^2) + eps):
     the codes, row absmax and outlier columns are those of quantize_rowwise(Y, threshold)
     (llmint8_add_rmsnorm_quantize). ``Y=False`` does not store Y (threshold <= 0 only; Y is
-    then returned as None). ``residual_out`` may be X or residual; without a residual it is
+    then returned as None, and the codes are those of ``torch.round(y * (127.0 / absmax))``, which
+    takes the reciprocal first). ``residual_out`` may be X or residual; without a residual it is
     X unless given. With find_outlier_cols the results are matmul_codes' inputs."""
     torch = _torch()
     index = _index(X, "X")
