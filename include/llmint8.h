@@ -438,7 +438,8 @@ LLMINT8_API llmint8_status llmint8_noalloc_read_status(int clear, uint32_t *out)
  * quantize the result's rows ([Q], [M]). X, residual, weight and residual_out
  * have the type `type`:
  *   h[i,c] = X[i,c] + residual[i,c], rounded to `type` (h = X without residual)
- *   y[i,c] = fp16( h[i,c] * weight[c] / sqrt(mean_c(h[i,:]^2) + eps) ), in fp32
+ *   y[i,c] = fp16( fp32( h[i,c] * weight[c] / sqrt(mean_c(h[i,:]^2) + eps) ) )
+ * with the value before the roundings as from 64 bits,
  * and codes, row_absmax and outlier_bitmap are exactly what
  * llmint8_quantize_rowwise(y, threshold) gives. Where Y is not asked for, the
  * multiplier of the codes is 127 * (1 / absmax) in place of 127 / absmax, each

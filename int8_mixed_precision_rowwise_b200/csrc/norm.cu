@@ -2,7 +2,7 @@
 // before an LLM.int8() linear, and the recovery of values from row codes.
 //
 //   h = x + residual, rounded to the input type (the new residual stream)
-//   y = fp16(h * rstd * w),  rstd = 1 / sqrt(mean(h^2) + eps) in fp32
+//   y = fp16(fp32(h * w / sqrt(mean(h^2) + eps))), as from 64 bits
 //   codes, row absmax, outlier bitmap of y: as llmint8_quantize_rowwise gives
 //   them for the stored y (page "Hugging Face 将 LLM.int8() 8-bit 量化集成进
 //   transformers 与 accelerate", sections "模型量化简介" and "MatMul 内部")
@@ -71,59 +71,201 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
     return r;
 }
 
+// Largest magnitudes of packed 16-bit values, NaN if one is.
 template <bool BF16>
-__device__ __forceinline__ void squares8(const uint4 &h, float2 &sum)
+__device__ __forceinline__ uint32_t top2(uint32_t a, uint32_t b)
 {
-    const uint32_t *a = reinterpret_cast<const uint32_t *>(&h);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float2 u = up2<BF16>(a[i]);
-        sum = fma2(u, u, sum);
+    if (BF16) {
+        const __nv_bfloat162 r = __hmax2_nan(__habs2(*reinterpret_cast<const __nv_bfloat162 *>(&a)),
+                                             __habs2(*reinterpret_cast<const __nv_bfloat162 *>(&b)));
+        return *reinterpret_cast<const uint32_t *>(&r);
     }
+    const __half2 r = __hmax2_nan(__habs2(*reinterpret_cast<const __half2 *>(&a)),
+                                  __habs2(*reinterpret_cast<const __half2 *>(&b)));
+    return *reinterpret_cast<const uint32_t *>(&r);
 }
 
-// y = fp16(h * w * rstd). The product of two 16-bit values is exact in fp32
-// (at most 22 significant bits), so y is off by rstd's error and one rounding.
+// Two fp32 values: what `hi` leaves of a sum or product is in `lo`.
+struct Pair {
+    float hi, lo;
+};
+
+__device__ __forceinline__ Pair operator+(Pair a, Pair b)
+{
+    const float s = __fadd_rn(a.hi, b.hi), t = __fsub_rn(s, a.hi);
+    const float left = __fadd_rn(__fsub_rn(a.hi, __fsub_rn(s, t)), __fsub_rn(b.hi, t)); // of a.hi + b.hi, exact
+    return {s, __fadd_rn(__fadd_rn(a.lo, b.lo), left)};
+}
+
+// y must come out as from 64 bits: one step of fp16 in y can move a code by
+// one, and a code's step is half of the values' rms in rows with a large
+// column. So the sum of squares and its root are pairs.
+//
+// Sum of the squares of a warp's vectors, N a thread, off by about 2^-38 of
+// itself, the same in all lanes. A square of 16-bit values is exact in fp32;
+// added to `acc`, which starts at a power of two above all of them, it splits
+// into what acc takes up and the rest, both exact. What acc took up is a whole
+// number of units, the rests nearly are of smaller ones, and whole numbers are
+// added over the warp by one instruction. NaN where the squares leave fp32's
+// range (of bf16 values), or for infinities and NaN.
+template <bool BF16, int N>
+__device__ __forceinline__ Pair warp_squares(const uint4 (&h)[N])
+{
+    uint32_t bits = 0u;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        bits = top2<BF16>(bits, top2<BF16>(top2<BF16>(h[i].x, h[i].y), top2<BF16>(h[i].z, h[i].w)));
+    bits = __reduce_max_sync(0xffffffffu, max(bits & 0xFFFFu, bits >> 16));
+    const float top = up2<BF16>(bits).x;
+    if (bits == 0u)
+        return {0.f, 0.f};
+    if (!(top > 1e-12f && top < 1e15f))
+        return {NAN, NAN};
+    const uint32_t start_exp = (__float_as_uint(top * top) >> 23) + 3u;
+    const float start = __uint_as_float(start_exp << 23), unit = __uint_as_float((start_exp - 23u) << 23);
+    const float per_unit = __uint_as_float((277u - start_exp) << 23);
+    float2 acc = make_float2(start, start), rest = make_float2(0.f, 0.f);
+    const float2 one = make_float2(1.f, 1.f), minus = make_float2(-1.f, -1.f);
+#pragma unroll
+    for (int i = 0; i < N * 4; ++i) {
+        const float2 u = up2<BF16>(reinterpret_cast<const uint32_t *>(h)[i]);
+        const float2 next = fma2(u, u, acc);
+        const float2 back = fma2(next, minus, acc); // what acc took up, negative
+        rest = fma2(fma2(u, u, back), one, rest);
+        acc = next;
+    }
+    // Of acc at most 2^25 units a component, so less than 2^31 in a warp.
+    const uint32_t n = __reduce_add_sync(0xffffffffu, (uint32_t)(__float2int_rn((acc.x - start) * per_unit) +
+                                                                 __float2int_rn((acc.y - start) * per_unit)));
+    const float r = rest.x + rest.y;
+    const uint32_t most = __reduce_max_sync(0xffffffffu, __float_as_uint(fabsf(r))) >> 23;
+    const uint32_t up = min(253u, 278u - most); // the rests times 2^(up - 127) are below 2^25
+    const int m = __reduce_add_sync(0xffffffffu, __float2int_rn(r * __uint_as_float(up << 23)));
+    const float nh = __uint2float_rn(n), nl = (float)(int)(n - (uint32_t)nh);
+    return {nh * unit, fmaf(nl, unit, (float)m * __uint_as_float((254u - up) << 23))};
+}
+
+// 1 / sqrt(mean + eps) as hi + lo, off by about 2^-40 of itself; `far`: where the
+// fp32 steps that use it could leave fp32's range, only `r` counts.
+struct RowScale {
+    float hi, lo;
+    bool far;
+    double r;
+};
+
+// One Newton step from fp32's root, with its error term as a pair.
+__device__ __forceinline__ RowScale row_scale(Pair sum, Pair inv_cols, float eps)
+{
+    const float mean = __fmul_rn(sum.hi, inv_cols.hi);
+    const float left = __fmaf_rn(sum.hi, inv_cols.hi, -mean);
+    Pair m = Pair{mean, __fadd_rn(left, __fmaf_rn(sum.hi, inv_cols.lo, __fmul_rn(sum.lo, inv_cols.hi)))} +
+             Pair{eps, 0.f};
+    const float whole = __fadd_rn(m.hi, m.lo); // m.lo may reach 2^-14 of m.hi
+    m = {whole, __fsub_rn(m.lo, __fsub_rn(whole, m.hi))};
+    const float r = rsqrtf(m.hi), q = __fmul_rn(r, r), ql = __fmaf_rn(r, r, -q);
+    const float p = __fmul_rn(m.hi, q), pl = __fmaf_rn(m.hi, q, -p);
+    const float e = __fsub_rn(__fsub_rn(__fsub_rn(1.f, p), pl), __fmaf_rn(m.hi, ql, __fmul_rn(m.lo, q)));
+    const float add = __fmul_rn(__fmul_rn(r, e), __fmaf_rn(0.375f, e, 0.5f));
+    const float hi = __uint_as_float(__float_as_uint(r) - 8u); // so that lo is above 0
+    return {hi, __fadd_rn(__fsub_rn(r, hi), add), !(m.hi > 1e-18f && m.hi < 1e18f), 0.0};
+}
+
 template <bool BF16>
-__device__ __forceinline__ uint4 norm8(const uint4 &h, const uint4 &w, float rstd)
+__device__ __noinline__ double squares_far(const uint4 h)
+{
+    double sum = 0.0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 u = up2<BF16>(reinterpret_cast<const uint32_t *>(&h)[i]);
+        sum += (double)u.x * u.x + (double)u.y * u.y;
+    }
+    return sum;
+}
+
+template <bool BF16>
+__device__ __noinline__ uint4 norm8_far(const uint4 h, const uint4 w, double r)
+{
+    uint4 o;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 a = up2<BF16>(reinterpret_cast<const uint32_t *>(&h)[i]);
+        const float2 b = up2<BF16>(reinterpret_cast<const uint32_t *>(&w)[i]);
+        reinterpret_cast<uint32_t *>(&o)[i] = down2<false>((float)((double)a.x * r * b.x), (float)((double)a.y * r * b.y));
+    }
+    return o;
+}
+
+// y = h * w / sqrt(mean(h^2) + eps), rounded to fp32 and then to fp16. The
+// product of two 16-bit values is exact in fp32 (at most 22 significant bits);
+// the second of its products with hi and lo is far below the first and the sum
+// is rounded once. An infinite product (of an infinite weight, or bf16 values)
+// stays one, as lo is above 0.
+template <bool BF16>
+__device__ __forceinline__ uint4 norm8(const uint4 &h, const uint4 &w, const RowScale &s)
 {
     const uint32_t *a = reinterpret_cast<const uint32_t *>(&h), *b = reinterpret_cast<const uint32_t *>(&w);
-    const float2 f = make_float2(rstd, rstd);
+    const float2 hi = make_float2(s.hi, s.hi), lo = make_float2(s.lo, s.lo);
     uint4 o;
     uint32_t *p = reinterpret_cast<uint32_t *>(&o);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const float2 y = mul2(mul2(up2<BF16>(a[i]), up2<BF16>(b[i])), f);
+        const float2 g = mul2(up2<BF16>(a[i]), up2<BF16>(b[i]));
+        const float2 y = fma2(g, hi, mul2(g, lo));
         p[i] = down2<false>(y.x, y.y);
     }
     return o;
 }
 
-template <bool MAX>
-__device__ __forceinline__ float warp_all(float v)
+// Of the block's warps, each lane one; lanes that are left over take one again
+// or `none`, so that all get the result.
+template <typename T, typename F>
+__device__ __forceinline__ T over_warps(T v, T *s, int nwarps, T none, F join)
 {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        const float u = __shfl_xor_sync(0xffffffffu, v, o);
-        v = MAX ? fmaxf(v, u) : v + u;
-    }
+    if (nwarps == 1)
+        return v;
+    if ((threadIdx.x & 31) == 0)
+        s[threadIdx.x >> 5] = v;
+    __syncthreads();
+    const int all = 1 << (32 - __clz(nwarps - 1)), from = threadIdx.x & (all - 1);
+    v = from < nwarps ? s[from] : none;
+    for (int o = 1; o < all; o <<= 1)
+        v = join(v, o);
     return v;
 }
 
-// Sum or maximum over the CTA, the same value in every thread. `s` holds one
-// float a warp; two buffers used in turn need no barrier between uses.
-template <bool MAX>
-__device__ __forceinline__ float block_all(float v, float *s, int nwarps)
+// Maximum of magnitudes, and sums, over the CTA, the same value in every thread.
+// `s` holds one value a warp; two buffers used in turn need no barrier between
+// uses.
+__device__ __forceinline__ float warp_max(float v)
 {
-    v = warp_all<MAX>(v);
+    return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(v, 0.f))));
+}
+
+__device__ __forceinline__ float block_max(float v, float *s, int nwarps)
+{
+    v = warp_max(v);
     if (nwarps == 1)
         return v;
     if ((threadIdx.x & 31) == 0)
         s[threadIdx.x >> 5] = v;
     __syncthreads();
     const int lane = threadIdx.x & 31;
-    v = lane < nwarps ? s[lane] : 0.f; // squares and magnitudes: 0 changes neither
-    return warp_all<MAX>(v);
+    return warp_max(lane < nwarps ? s[lane] : 0.f);
+}
+
+__device__ __forceinline__ Pair block_sum(Pair v, Pair *s, int nwarps)
+{
+    return over_warps(v, s, nwarps, Pair{0.f, 0.f}, [](Pair a, int o) {
+        return a + Pair{__shfl_xor_sync(0xffffffffu, a.hi, o), __shfl_xor_sync(0xffffffffu, a.lo, o)};
+    });
+}
+
+__device__ __noinline__ double block_sum_far(double v, double *s, int nwarps)
+{
+    auto join = [](double a, int o) { return a + __shfl_xor_sync(0xffffffffu, a, o); };
+    for (int o = 1; o < 32; o <<= 1)
+        v = join(v, o);
+    return over_warps(v, s, nwarps, 0.0, join);
 }
 
 // What a row's values are multiplied with before they are rounded to codes:
@@ -145,10 +287,17 @@ struct NormParams {
     float *absmax;
     int64_t rows;
     int cols;
-    float eps, inv_cols;
+    float eps;
+    Pair inv_cols;
     __half t16;
     uint32_t *sets, *calls, *sync, *grown, *bitmap_out, *status;
 };
+
+// The scale of a row that is `far`.
+__device__ __noinline__ double root_far(double sum, int cols, float eps)
+{
+    return 1.0 / sqrt(sum / cols + eps);
+}
 
 constexpr int kListed = 1024; // outlier columns that the fix-up visits one by one
 
@@ -250,7 +399,7 @@ __device__ __forceinline__ void fix_rows(const NormParams &p, int64_t first, int
                 __half2 a[4];
                 m2 = __hmax2(m2, vec_abs_max(v, a));
             }
-            const float amax = block_all<true>(fmaxf(__low2float(m2), __high2float(m2)), s_max, nwarps);
+            const float amax = block_max(fmaxf(__low2float(m2), __high2float(m2)), s_max, nwarps);
             const float s = code_multiplier(amax, false);
             for (int c = tid; c < nvec; c += blockDim.x) {
                 uint4 v = yr[c];
@@ -274,7 +423,9 @@ __device__ __forceinline__ void fix_rows(const NormParams &p, int64_t first, int
 template <bool BF16, bool THR, int MAXT>
 __global__ void __launch_bounds__(MAXT, 1024 / MAXT) k_norm_quant(const NormParams p)
 {
-    __shared__ float s_red[3][32];
+    __shared__ float s_red[2][32];
+    __shared__ Pair s_sum[32];
+    __shared__ double s_far[32];
     extern __shared__ uint32_t s_dyn[]; // THR: the set, then its listed columns
     const int tid = threadIdx.x, nwarps = blockDim.x >> 5;
     const int nvec = p.cols >> 3;
@@ -337,12 +488,14 @@ __global__ void __launch_bounds__(MAXT, 1024 / MAXT) k_norm_quant(const NormPara
                     known |= ((__ldcg(set + (c >> 2)) >> ((c & 3) * 8)) & 0xFFu) << (8 * i);
             }
         }
-        float2 ss2 = make_float2(0.f, 0.f);
+        RowScale scale = row_scale(block_sum(warp_squares<BF16>(v), s_sum, nwarps), p.inv_cols, p.eps);
+        if (scale.far) { // the same in all threads
+            double sum = 0.0;
 #pragma unroll
-        for (int i = 0; i < kVec; ++i)
-            squares8<BF16>(v[i], ss2);
-        const float ss = block_all<false>(ss2.x + ss2.y, s_red[0], nwarps);
-        const float rstd = rsqrtf(fmaf(ss, p.inv_cols, p.eps));
+            for (int i = 0; i < kVec; ++i)
+                sum += squares_far<BF16>(v[i]);
+            scale.r = root_far(block_sum_far(sum, s_far, nwarps), p.cols, p.eps);
+        }
         if (p.h) {
             uint4 *hr = p.h + r * nvec;
 #pragma unroll
@@ -352,12 +505,21 @@ __global__ void __launch_bounds__(MAXT, 1024 / MAXT) k_norm_quant(const NormPara
                     hr[c] = v[i];
             }
         }
+        if (scale.far) {
+#pragma unroll
+            for (int i = 0; i < kVec; ++i) {
+                const int c = tid + i * blockDim.x;
+                if (c < nvec)
+                    v[i] = norm8_far<BF16>(v[i], __ldg(p.w + c), scale.r);
+            }
+        }
         __half2 m2 = __float2half2_rn(0.f);
 #pragma unroll
         for (int i = 0; i < kVec; ++i) {
             const int c = tid + i * blockDim.x;
             if (c < nvec) {
-                v[i] = norm8<BF16>(v[i], __ldg(p.w + c), rstd);
+                if (!scale.far)
+                    v[i] = norm8<BF16>(v[i], __ldg(p.w + c), scale);
                 if (p.y)
                     p.y[r * nvec + c] = v[i];
                 __half2 a[4];
@@ -378,7 +540,7 @@ __global__ void __launch_bounds__(MAXT, 1024 / MAXT) k_norm_quant(const NormPara
                 m2 = __hmax2(m2, m);
             }
         }
-        amax = block_all<true>(fmaxf(__low2float(m2), __high2float(m2)), s_red[1], nwarps);
+        amax = block_max(fmaxf(__low2float(m2), __high2float(m2)), s_red[0], nwarps);
         const float s = code_multiplier(amax, !THR && !p.y);
 #pragma unroll
         for (int i = 0; i < kVec; ++i) {
@@ -411,7 +573,7 @@ __global__ void __launch_bounds__(MAXT, 1024 / MAXT) k_norm_quant(const NormPara
         }
         r -= gridDim.x; // this CTA's last row
         if (__syncthreads_or(more)) {
-            amax = block_all<true>(fmaxf(__low2float(m2), __high2float(m2)), s_red[2], nwarps);
+            amax = block_max(fmaxf(__low2float(m2), __high2float(m2)), s_red[1], nwarps);
             const float s = code_multiplier(amax, false);
 #pragma unroll
             for (int i = 0; i < kVec; ++i) {
@@ -435,7 +597,9 @@ __global__ void __launch_bounds__(MAXT, 1024 / MAXT) k_norm_quant(const NormPara
 template <bool BF16, bool THR>
 __global__ void __launch_bounds__(kMaxRowThreads, 1) k_norm_quant_wide(const NormParams p)
 {
-    __shared__ float s_red[2][32];
+    __shared__ float s_red[32];
+    __shared__ Pair s_sum[32];
+    __shared__ double s_far[32];
     extern __shared__ uint32_t s_words[];
     const int tid = threadIdx.x, nwarps = blockDim.x >> 5;
     const int nvec = p.cols >> 3;
@@ -447,20 +611,31 @@ __global__ void __launch_bounds__(kMaxRowThreads, 1) k_norm_quant_wide(const Nor
         set = p.sets + (call & 1u) * kSetWords;
     }
     for (int64_t r = blockIdx.x; r < p.rows; r += gridDim.x) {
-        float2 ss2 = make_float2(0.f, 0.f);
         auto hidden = [&](int c) {
             uint4 v = p.x[r * nvec + c];
             if (p.res)
                 v = add8<BF16>(v, p.res[r * nvec + c]);
             return v;
         };
-        for (int c = tid; c < nvec; c += blockDim.x)
-            squares8<BF16>(hidden(c), ss2);
-        const float ss = block_all<false>(ss2.x + ss2.y, s_red[0], nwarps);
-        const float rstd = rsqrtf(fmaf(ss, p.inv_cols, p.eps));
+        Pair squares{0.f, 0.f};
+        for (int c0 = 0; c0 < nvec; c0 += blockDim.x) { // whole warps
+            const uint4 h[1] = {c0 + tid < nvec ? hidden(c0 + tid) : make_uint4(0, 0, 0, 0)};
+            squares = squares + warp_squares<BF16>(h);
+        }
+        RowScale scale = row_scale(block_sum(squares, s_sum, nwarps), p.inv_cols, p.eps);
+        if (scale.far) { // the same in all threads
+            double sum = 0.0;
+            for (int c = tid; c < nvec; c += blockDim.x)
+                sum += squares_far<BF16>(hidden(c));
+            scale.r = root_far(block_sum_far(sum, s_far, nwarps), p.cols, p.eps);
+        }
+        auto normed = [&](const uint4 &h, int c) {
+            const uint4 w = __ldg(p.w + c);
+            return scale.far ? norm8_far<BF16>(h, w, scale.r) : norm8<BF16>(h, w, scale);
+        };
         __half2 m2 = __float2half2_rn(0.f);
         for (int c = tid; c < nvec; c += blockDim.x) {
-            uint4 v = norm8<BF16>(hidden(c), __ldg(p.w + c), rstd);
+            uint4 v = normed(hidden(c), c);
             __half2 a[4];
             if (THR) {
                 const uint32_t hit = hit_mask8(v, p.t16);
@@ -471,13 +646,13 @@ __global__ void __launch_bounds__(kMaxRowThreads, 1) k_norm_quant_wide(const Nor
             }
             m2 = __hmax2(m2, vec_abs_max(v, a));
         }
-        const float amax = block_all<true>(fmaxf(__low2float(m2), __high2float(m2)), s_red[1], nwarps);
+        const float amax = block_max(fmaxf(__low2float(m2), __high2float(m2)), s_red, nwarps);
         const float s = code_multiplier(amax, !THR && !p.y);
         // h may take the place of x or the residual: it is stored last, each
         // vector by the thread that read it.
         for (int c = tid; c < nvec; c += blockDim.x) {
             const uint4 h = hidden(c);
-            uint4 v = norm8<BF16>(h, __ldg(p.w + c), rstd);
+            uint4 v = normed(h, c);
             if (p.h)
                 p.h[r * nvec + c] = h;
             if (p.y)
@@ -494,7 +669,7 @@ __global__ void __launch_bounds__(kMaxRowThreads, 1) k_norm_quant_wide(const Nor
         int *s_col = reinterpret_cast<int *>(s_words + ((p.cols + 31) >> 5));
         const int count = complete_set(p, call, s_set, s_col);
         if (count > 0)
-            fix_rows(p, blockIdx.x, p.rows, count, s_set, s_col, s_red[0]);
+            fix_rows(p, blockIdx.x, p.rows, count, s_set, s_col, s_red);
     }
 }
 
@@ -553,7 +728,8 @@ cudaError_t launch_norm_quant(const NormArgs &a, const Workspace &ws, const Devi
     p.rows = a.rows;
     p.cols = (int)a.cols;
     p.eps = a.eps;
-    p.inv_cols = (float)(1.0 / (double)a.cols);
+    p.inv_cols.hi = (float)(1.0 / (double)a.cols);
+    p.inv_cols.lo = (float)(1.0 / (double)a.cols - (double)p.inv_cols.hi);
     p.t16 = threshold_fp16(a.t);
     p.sets = ws.sets;
     p.calls = ws.calls;
