@@ -37,9 +37,9 @@ __device__ __forceinline__ SeqShape seq_shape(const AttnParams &p, int b)
 {
     const KvView &c = p.c;
     SeqShape s;
-    const int begin = __ldg(c.cu + b), end = __ldg(c.cu + b + 1);
+    const int begin = c.cu[b], end = c.cu[b + 1];
     s.n = begin >= 0 && end > begin && end <= p.tokens ? end - begin : 0;
-    s.len = max(0, __ldg(c.lens + b));
+    s.len = max(0, c.lens[b]);
     s.keys = min(s.len, c.table_width << c.page_shift);
     s.rows = (int)min((int64_t)s.n * p.group, (int64_t)INT32_MAX);
     const bool mine = s.rows >= p.rows_from && s.rows <= p.rows_to;
@@ -258,7 +258,7 @@ struct LoadWalk {
         u.first = c == q.c0;
         const int j = key >> kv.page_shift;
         if (u.want && j < kv.table_width)
-            u.page = __ldg(kv.table + q.b * kv.table_stride + j);
+            u.page = kv.table[q.b * kv.table_stride + j];
         u.h = q.h;
         u.slot = key & (kv.page_size - 1);
         ++c;
@@ -270,7 +270,7 @@ struct LoadWalk {
             bad = true;
             u.page = -1;
         }
-        u.scale = u.page >= 0 ? __ldg(((threadIdx.x & 31) >= 8 ? kv.va : kv.ka) + (u.page * kv.heads + u.h)) : 0.f;
+        u.scale = u.page >= 0 ? __ldcg(((threadIdx.x & 31) >= 8 ? kv.va : kv.ka) + (u.page * kv.heads + u.h)) : 0.f;
     }
 };
 

@@ -213,7 +213,7 @@ __global__ void __launch_bounds__(Smem<D, NQ>::kThreads, Smem<D, NQ>::kCtas)
         uint32_t qb[NQ][KS][2];
         float fac[NQ][2], slope[NQ][2];
         int limit[NQ][2], pos[NQ][2]; // last key a row sees
-        const int64_t first_row = __ldg(c.cu + q.b);
+        const int64_t first_row = c.cu[q.b];
 #pragma unroll
         for (int i = 0; i < NQ; ++i) {
             const int row = g + 8 * i;
@@ -226,7 +226,7 @@ __global__ void __launch_bounds__(Smem<D, NQ>::kThreads, Smem<D, NQ>::kCtas)
             uint32_t w[2 * KS];
 #pragma unroll
             for (int v = 0; v < KS / 2; ++v)
-                reinterpret_cast<uint4 *>(w)[v] = live ? __ldg(src + v) : make_uint4(0, 0, 0, 0);
+                reinterpret_cast<uint4 *>(w)[v] = live ? src[v] : make_uint4(0, 0, 0, 0);
             float f = 1.f;
             if (p.bf16)
                 f = bf16_to_f16<4>(w);

@@ -286,7 +286,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_prefill(const __grid_const
                 // as that takes; a row's place comes from the lane that has it.
                 constexpr int kLanes = D / 8, kSteps = kLanes;
                 const uint64_t src = reinterpret_cast<uint64_t>(
-                    static_cast<const uint16_t *>(p.q) + (__ldg(c.cu + info->b) + (int64_t)tok) * p.q_token +
+                    static_cast<const uint16_t *>(p.q) + (c.cu[info->b] + (int64_t)tok) * p.q_token +
                     head * p.q_head);
                 const uint32_t flip = p.scale_log2 < 0.f ? 0x80008000u : 0u; // scores grow with the products
                 uint4 w[kSteps];
@@ -295,7 +295,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_prefill(const __grid_const
                     const int from = k * (32 / kLanes) + lane / kLanes;
                     const uint64_t at = __shfl_sync(0xffffffffu, src, from);
                     const bool there = __shfl_sync(0xffffffffu, (int)live, from);
-                    w[k] = there ? __ldg(reinterpret_cast<const uint4 *>(at) + lane % kLanes) : make_uint4(0, 0, 0, 0);
+                    w[k] = there ? reinterpret_cast<const uint4 *>(at)[lane % kLanes] : make_uint4(0, 0, 0, 0);
                 }
 #pragma unroll
                 for (int k = 0; k < kSteps; ++k) {
@@ -438,7 +438,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_prefill(const __grid_const
             // ---- the segment's sums out
             const int c1 = key / kUnit + 1; // its units are [c0, c1) of the item
             const bool whole = info->whole;
-            const int64_t out_row = (int64_t)__ldg(c.cu + info->b) * p.heads;
+            const int64_t out_row = (int64_t)c.cu[info->b] * p.heads;
             // An item's first part goes to the CTA's second slot.
             const int64_t begin = walked - c1; // of the item
             float *part = p.slots + ((int64_t)blockIdx.x * 2 + (begin >= range.u0 ? 1 : 0)) * (kRows * (D + 2));

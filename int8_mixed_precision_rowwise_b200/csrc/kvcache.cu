@@ -76,9 +76,9 @@ __device__ __forceinline__ void find_places(const KvView &c, int64_t t0, int n, 
         const int64_t t = t0 + i;
         const int b = i < n && t < tokens ? sequence_of(c, t) : -1;
         if (b >= 0) {
-            begin = __ldg(c.cu + b);
-            end = __ldg(c.cu + b + 1);
-            const int64_t pos = (int64_t)__ldg(c.lens + b) - (end - t);
+            begin = c.cu[b];
+            end = c.cu[b + 1];
+            const int64_t pos = (int64_t)c.lens[b] - (end - t);
             if (t >= begin && t < end && pos >= 0) { // offsets that decrease have no rows
                 page = page_of(c, b, (int)pos);
                 slot = (int)pos & (c.page_size - 1);
@@ -131,21 +131,21 @@ __global__ void __launch_bounds__(kHeads * 32, 4) k_kv_append(const AppendParams
         const int64_t block = (int64_t)page * c.heads + h;
         float *scale = (kv ? c.va : c.ka) + block;
         int8_t *dst = (kv ? c.v : c.k) + block * c.page_size * D;
-        const float old = slot ? *scale : 0.f;
+        const float old = slot ? __ldcg(scale) : 0.f;
         const uint4 *rows = src + t * step;
         uint4 held[kHeld];
         uint32_t bits = 0u;
 #pragma unroll
         for (int k = 0; k < kHeld; ++k) {
             const int r = row + k * kRows;
-            held[k] = r < len ? __ldg(rows + r * step) : make_uint4(0, 0, 0, 0);
+            held[k] = r < len ? rows[r * step] : make_uint4(0, 0, 0, 0);
         }
 #pragma unroll
         for (int k = 0; k < kHeld; ++k)
             bits = max_bits8(bits, held[k]);
 #pragma unroll 8
         for (int r = 16 + row; r < len; r += kRows)
-            bits = max_bits8(bits, __ldg(rows + r * step));
+            bits = max_bits8(bits, rows[r * step]);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1)
             bits = __vmaxu2(bits, __shfl_xor_sync(0xffffffffu, bits, o));
@@ -172,9 +172,16 @@ __global__ void __launch_bounds__(kHeads * 32, 4) k_kv_append(const AppendParams
             if (r < len)
                 to[r * (D / 8)] = kv_codes8<BF16>(held[k], m);
         }
-#pragma unroll 4
-        for (int r = 16 + row; r < len; r += kRows)
-            to[r * (D / 8)] = kv_codes8<BF16>(__ldg(rows + r * step), m);
+        for (int r0 = 16 + row; r0 < len; r0 += 4 * kRows) {
+            uint4 u[4]; // all under way before the first is stored
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                u[k] = r0 + k * kRows < len ? rows[(r0 + k * kRows) * step] : make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (r0 + k * kRows < len)
+                    to[(r0 + k * kRows) * (D / 8)] = kv_codes8<BF16>(u[k], m);
+        }
         __syncwarp();
         if (lane == 0)
             *scale = amax;
@@ -208,8 +215,8 @@ __global__ void __launch_bounds__(256, 4) k_kv_read(const KvView c, uint4 *k_out
                 const int e = pair + i * kTokens, r = e % kWindow, h = h0 + e / kWindow;
                 if (s.page[r] >= 0 && h < c.heads) {
                     const int block = s.page[r] * c.heads + h; // fits: pages * heads * page_size < 2^31
-                    v[i] = __ldg(codes + ((int64_t)(block * c.page_size + s.slot[r])) * kPieces + x);
-                    f[i] = __ldg(absmax + block);
+                    v[i] = __ldcg(codes + ((int64_t)(block * c.page_size + s.slot[r])) * kPieces + x);
+                    f[i] = __ldcg(absmax + block);
                 }
             }
 #pragma unroll

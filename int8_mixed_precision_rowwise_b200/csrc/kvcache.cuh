@@ -9,7 +9,9 @@
 
 namespace llmint8 {
 
-// The cache and its sequences as the kernels see them.
+// The cache and its sequences as the kernels see them. The kernel before may
+// write any of it while this one starts: no loads that take it as constant
+// (__ldg), and absmax, whose lines are written by several CTAs, past L1 (__ldcg).
 struct KvView {
     int8_t *k, *v;
     float *ka, *va;
@@ -24,11 +26,11 @@ struct KvView {
 __device__ __forceinline__ int sequence_of(const KvView &c, int64_t t)
 {
     int lo = 0, hi = c.batch; // cu[lo] <= t < cu[hi], if t has a sequence
-    if (t < __ldg(c.cu) || t >= __ldg(c.cu + c.batch))
+    if (t < c.cu[0] || t >= c.cu[c.batch])
         return -1;
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (__ldg(c.cu + mid) <= t)
+        if (c.cu[mid] <= t)
             lo = mid;
         else
             hi = mid;
@@ -43,7 +45,7 @@ __device__ __forceinline__ int page_of(const KvView &c, int b, int pos)
     const int j = pos >> c.page_shift;
     int page = -1;
     if (j < c.table_width)
-        page = __ldg(c.table + b * c.table_stride + j);
+        page = c.table[b * c.table_stride + j];
     if ((unsigned)page >= (unsigned)c.pages) {
         atomicOr(c.status, LLMINT8_DEV_BAD_PAGE);
         page = -1;

@@ -677,9 +677,8 @@ __global__ void __launch_bounds__(kMaxRowThreads, 1) k_norm_quant_wide(const Nor
 // width apart: 8-byte loads, all under way at once, and whole sectors stored. A
 // vector's row is carried along, not divided for.
 template <bool BF16>
-__global__ void __launch_bounds__(256) k_dequant_rows(const uint2 *__restrict__ codes,
-                                                      const float *__restrict__ absmax, int64_t n8, int row8,
-                                                      uint4 *__restrict__ out)
+__global__ void __launch_bounds__(256) k_dequant_rows(const uint2 *codes, const float *absmax, int64_t n8, int row8,
+                                                      uint4 *out)
 {
     griddep_wait();
     griddep_release();
@@ -693,7 +692,7 @@ __global__ void __launch_bounds__(256) k_dequant_rows(const uint2 *__restrict__ 
         for (int k = 0; k < 4; ++k) {
             if (i0 + k * 256 < n8) {
                 c[k] = __ldcs(codes + i0 + k * 256);
-                s[k] = __ldg(absmax + row);
+                s[k] = absmax[row];
             }
             row += dr;
             col += dc;
