@@ -473,6 +473,7 @@ llmint8_status llmint8_gemm_s8s8s32(const int8_t *A, int64_t M, const int8_t *B,
     g.epi = Epilogue::RawInt32;
     g.Y = acc;
     g.status = ws.status;
+    g.fresh_b = true;
     return cuda_status(launch_gemm(g, dev, stream));
 }
 

@@ -70,6 +70,7 @@ struct KParams {
     // row, zx the zero point, rsum the code row sums of W.
     const int32_t *zx, *rsum;
     int out_f32;               // MixedFp16 epilogue: store fp32 (1) instead of fp16 (0)
+    int fresh_b;               // the weight operand may come from the kernel before: wait before reading it
     // Gathered outlier operands (null: gathered in place): W's outlier columns
     // [kGatherCols x np] and SB [np] (staged per tile by bulk copies), X's
     // outlier columns [kGatherCols x mp] (read per row).
@@ -905,6 +906,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             // queueing its few reads behind the flood.)
             const CUtensorMap *wmap = SWAP ? &tmA : &tmB;
             int pre = 0;
+            if (p.fresh_b)
+                griddep_wait();
             if ((int)blockIdx.x < num_tiles) {
                 const int mb = (int)blockIdx.x % p.num_m_blk, nb = (int)blockIdx.x / p.num_m_blk;
                 const int wrow = SWAP ? mb * BM : nb * BN;
@@ -1134,6 +1137,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
             // The weight half (B) of the first stages goes out before the wait
             // for the quantizer's codes (A).
             int pre = 0;
+            if (p.fresh_b)
+                griddep_wait();
             if (nwork > 0) {
                 const Seg f = sc.item(0);
                 const int nb = f.tile / p.num_m_blk;
@@ -1486,6 +1491,7 @@ cudaError_t run(const GemmArgs &a, const DeviceInfo &dev, cudaStream_t stream)
     p.zx = a.zx;
     p.rsum = a.rsum;
     p.out_f32 = a.out_f32;
+    p.fresh_b = a.fresh_b ? 1 : 0;
     p.wt_t = SWAP ? nullptr : a.wt_t;
     p.sb_p = a.sb_p;
     p.xo_t = a.xo_t;
@@ -1537,6 +1543,7 @@ cudaError_t run_pair(const GemmArgs &a, const DeviceInfo &dev, cudaStream_t stre
     p.zx = a.zx;
     p.rsum = a.rsum;
     p.out_f32 = a.out_f32;
+    p.fresh_b = a.fresh_b ? 1 : 0;
     p.wt_t = a.wt_t;
     p.sb_p = a.sb_p;
     p.xo_t = a.xo_t;

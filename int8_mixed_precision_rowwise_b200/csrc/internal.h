@@ -258,6 +258,9 @@ struct GemmArgs {
     // MixedFp16 epilogue only: 1 stores Y as fp32 [M x N] (a partial sum of a
     // tensor-parallel row split), 0 as fp16.
     int out_f32;
+    // Set where the kernel before in the stream may be the one that writes B (a
+    // call of the GEMM alone; behind a quantizer of X, B is complete).
+    bool fresh_b;
     // Gathered outlier operands (launch_gather_outliers; null: the epilogue
     // gathers W's and X's outlier values in place).
     const float *wt_t, *sb_p, *xo_t;

@@ -234,6 +234,7 @@ llmint8_status llmint8_matmul_codes(const int8_t *CX, const float *SX, const voi
     g.epi = Epilogue::MixedFp16;
     g.Y = Y;
     g.out_f32 = out_dtype == LLMINT8_OUT_F32 ? 1 : 0;
+    g.fresh_b = true;
     return launch_gemm(g, dev, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? LLMINT8_OK
                                                                                        : LLMINT8_ERR_CUDA;
 }
