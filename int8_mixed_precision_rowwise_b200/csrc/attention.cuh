@@ -275,9 +275,9 @@ struct LoadWalk {
 };
 
 // What the scores need of a 16-key group, by its two lanes: the keys' scale in
-// log2 units, log2 of the values' scale and its inverse. A group without a
-// page weighs nothing: scale 0, weight 2^-inf.
-__device__ __forceinline__ void store_meta(float *meta, const UnitLoad &u, float scale_log2)
+// log2 units, log2 of the values' scale and its inverse, over what the weights
+// start at. A group without a page weighs nothing: scale 0, weight 2^-inf.
+__device__ __forceinline__ void store_meta(float *meta, const UnitLoad &u, float scale_log2, float start)
 {
     const int lane = threadIdx.x & 31;
     if (lane < 8) {
@@ -285,7 +285,7 @@ __device__ __forceinline__ void store_meta(float *meta, const UnitLoad &u, float
     } else if (lane < 16) {
         const float vs = fmaxf(u.scale * (1.0f / 127.0f), 1e-30f);
         meta[1] = u.page >= 0 ? log2f(vs) : -INFINITY;
-        meta[2] = u.page >= 0 ? 1.0f / vs : 0.f;
+        meta[2] = u.page >= 0 ? 1.0f / vs / start : 0.f;
     }
 }
 
@@ -392,14 +392,15 @@ __device__ __forceinline__ void add_part(float &M, float &l, float4 &acc, float2
 }
 
 // Four output values of row R (token R / group, head h * group + R % group) of
-// a sequence whose rows start at out_row / heads, and its lse.
+// a sequence whose rows start at out_row / heads, and its lse. The values are
+// weighted with what the weights start at, their sum l is not.
 template <int D>
 __device__ __forceinline__ void finish_row(const AttnParams &p, int64_t out_row, int h, int R, int chunk, float4 acc,
-                                           float M, float l)
+                                           float M, float l, float start)
 {
     const int tok = R / p.group, head = h * p.group + (R - tok * p.group);
     const int64_t row = out_row + (int64_t)tok * p.heads + head;
-    const float inv = l > 0.f ? 1.0f / l : 0.f;
+    const float inv = l > 0.f ? 1.0f / l / start : 0.f;
     uint2 v;
     if (p.bf16)
         v = make_uint2(down2<true>(acc.x * inv, acc.y * inv), down2<true>(acc.z * inv, acc.w * inv));

@@ -6,14 +6,17 @@
 // Mathematics. With codes kc, vc (exact as fp16), page scales ka / 127 and
 // va / 127, and everything per key in log2 units:
 //   x_j = (q . kc_j) * (ka_j / 127 * scale * log2 e) [+ slope * (j - p) * log2 e]
-//   e_j = x_j + log2(va_j / 127),  w_j = 2^(e_j - m),  m the running maximum of e
-//   o = sum_j w_j vc_j,  l = sum_j w_j * (127 / va_j),  out = o / l
+//   e_j = x_j + log2(va_j / 127),  w_j = 2^(e_j - m + 8),  m the running maximum of e
+//   o = sum_j w_j vc_j,  l = sum_j w_j * (127 / va_j) / 2^8,  out = o / 2^8 / l
 // The value scale rides on the exponent, so that the weights that enter the
-// product are at most 1 (no overflow of fp16) and the codes stay exact.
+// product are about 2^8 at most (no overflow of fp16) and the codes stay exact.
+// They start there and not at 1 because fp16 ends at 2^-24: in a long sequence
+// with one heavy key all others weigh little.
 // q . kc and w . vc run on the tensor cores (fp16 in, fp32 sums). With row
 // tiles of 8 the weights enter as hi + lo, what rounding to fp16 left over in
-// a second product: there the matrix instructions have time to spare. With 16
-// rows the weights are fp16 (off by at most 2^-11 of themselves).
+// a second product (off by at most 2^-22 of themselves or 2^-33 of the largest):
+// there the matrix instructions have time to spare. With 16 rows the weights
+// are fp16 (off by at most 2^-11 of themselves, or 2^-33 of the largest).
 //
 // Work. Unit: 128 keys of one (sequence, head, row tile). The units of all of
 // them in order are split evenly over the CTAs, whatever the lengths; a CTA
@@ -56,7 +59,8 @@ constexpr int kWarps = 4;             // that compute
 constexpr int kSub = 32;              // keys a warp takes at once
 constexpr int kUnit = kSub * kWarps;  // keys of a unit
 constexpr int kGroups = kUnit / 16;   // 16 keys lie in one page
-constexpr float kSlack = 6.f;         // log2 of how far a weight may exceed 1
+constexpr float kStart = 8.f;         // log2 of the weight at the running maximum
+constexpr float kSlack = 6.f;         // log2 of how far a weight may exceed that: 2^14 at most, fp16 holds it
 
 // With row tiles of 8 the registers allow three CTAs an SM, with 16 two; the
 // ring takes what shared memory that leaves (192 KB an SM either way).
@@ -184,7 +188,7 @@ __global__ void __launch_bounds__(Smem<D, NQ>::kThreads, Smem<D, NQ>::kCtas)
             if (load)
                 tma_load_2d(ring + (s * 2 + (is_v ? 1 : 0)) * kTile + group * 16 * D, is_v ? &vm : &km, bar, 0,
                             ((u0.page * c.heads + u0.h) << page_shift) + u0.slot);
-            store_meta(s_meta + (s * kGroups + group) * 4, u0, p.scale_log2);
+            store_meta(s_meta + (s * kGroups + group) * 4, u0, p.scale_log2, exp2f(kStart));
             __syncwarp();
             if (lane == 0)
                 mbar_arrive(bar);
@@ -348,7 +352,8 @@ __global__ void __launch_bounds__(Smem<D, NQ>::kThreads, Smem<D, NQ>::kCtas)
                             }
                         }
                     }
-                    const float mu[2] = {m[i][0] == -INFINITY ? 0.f : m[i][0], m[i][1] == -INFINITY ? 0.f : m[i][1]};
+                    const float mu[2] = {(m[i][0] == -INFINITY ? 0.f : m[i][0]) - kStart,
+                                         (m[i][1] == -INFINITY ? 0.f : m[i][1]) - kStart};
 #pragma unroll
                     for (int a = 0; a < 2; ++a) {
                         const float iv = a ? m1.z : m0.z;
@@ -457,7 +462,7 @@ __global__ void __launch_bounds__(Smem<D, NQ>::kThreads, Smem<D, NQ>::kCtas)
                         acc.w = fmaf(v.w, f, acc.w);
                     }
                     if (whole) {
-                        finish_row<D>(p, out_row, q.h, q.row0 + row, ch, acc, M, lsum);
+                        finish_row<D>(p, out_row, q.h, q.row0 + row, ch, acc, M, lsum, exp2f(kStart));
                     } else {
                         reinterpret_cast<float4 *>(slot)[row * (D / 4) + ch] = acc;
                         if (ch == 0)
@@ -494,7 +499,7 @@ __global__ void __launch_bounds__(Smem<D, NQ>::kThreads, Smem<D, NQ>::kCtas)
                         const float4 v = __ldcg(reinterpret_cast<const float4 *>(part) + row * (D / 4) + ch);
                         add_part(M, lsum, acc, ml, v);
                     }
-                    finish_row<D>(p, out_row, q.h, q.row0 + row, ch, acc, M, lsum);
+                    finish_row<D>(p, out_row, q.h, q.row0 + row, ch, acc, M, lsum, exp2f(kStart));
                 }
             }
             named_barrier_sync(1, kWarps * 32);

@@ -552,7 +552,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_prefill(const __grid_const
 #pragma unroll
                         for (int x = 0; x < kAt; ++x)
                             if (r0 + x * kStep < rows)
-                                finish_row<D>(p, out_row, h, row0 + r0 + x * kStep, ch, acc[x], M[x], lsum[x]);
+                                finish_row<D>(p, out_row, h, row0 + r0 + x * kStep, ch, acc[x], M[x], lsum[x], 1.f);
                     }
                 }
                 sync(); // s_last is free
@@ -733,7 +733,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_prefill(const __grid_const
                 units.scale(p, u1);
                 if (lane == 0)
                     s_info[i % kMetaRing].last = !u1.some || u1.first;
-                store_meta(s_meta + ((i % kMetaRing) * kGroups + group) * 4, u0, fabsf(p.scale_log2));
+                store_meta(s_meta + ((i % kMetaRing) * kGroups + group) * 4, u0, fabsf(p.scale_log2), 1.f);
                 const bool load = loads && u0.page >= 0;
                 const uint32_t which = __ballot_sync(0xffffffffu, load);
                 __syncwarp(); // all lanes' scales are written

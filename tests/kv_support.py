@@ -79,8 +79,10 @@ def sequence_values(codes, absmax, table_row, length, head):
         (absmax[ids, head].double() / 127).repeat_interleave(page)[:length]
 
 
-def attention_reference(Q, k, v, ka, va, table, lens, news, scale, causal=True, slopes=None):
-    """(out, lse, bound of |out's error| before its own rounding) in float64, for packed rows Q."""
+def attention_reference(Q, k, v, ka, va, table, lens, news, scale, causal=True, slopes=None, weight=2.0 ** -11,
+                        least=2.0 ** -25):
+    """(out, lse, bound of |out's error| before its own rounding) in float64, for packed rows Q. A weight enters the
+    value product off by ``weight`` of itself or ``least`` of the row's largest."""
     T, H, D = Q.shape
     group = H // k.shape[1]
     out = torch.zeros((T, H, D), dtype=torch.float64, device=Q.device)
@@ -112,13 +114,14 @@ def attention_reference(Q, k, v, ka, va, table, lens, news, scale, causal=True, 
             p = torch.where(some[:, None], torch.softmax(s, 1), 0.0).nan_to_num(0.0)
             ds = torch.where(seen, ds, 0.0)
             # a weight is off by its score's error, the exponential's and the score scaling's few units of 2^-24 of
-            # |s|, half a step of fp16; weights below fp16's range relative to the row's largest lose 2^-25 of it
+            # |s|, half a step of fp16 (`weight`); weights below fp16's range relative to the row's largest lose 2^-25
+            # of it (`least`)
             mag = torch.where(seen, s.abs(), 0.0).amax(1, keepdim=True)
-            rel = 2.0 ** -11 + 2 * (ds.amax(1, keepdim=True) + mag * 2.0 ** -21 + 2.0 ** -19)
+            rel = weight + 2 * (ds.amax(1, keepdim=True) + mag * 2.0 ** -21 + 2.0 ** -19)
             w = (p * vs[None]).amax(1, keepdim=True)
             o = p @ V
             out[t0:t0 + n, h] = o
-            tol[t0:t0 + n, h] = rel * (p @ V.abs()) + rel * o.abs() + 2.0 ** -25 * 127 * length * w
+            tol[t0:t0 + n, h] = rel * (p @ V.abs()) + rel * o.abs() + least * 127 * length * w
             lse[t0:t0 + n, h] = torch.where(some, torch.logsumexp(s, 1), -float("inf"))
         t0 += n
     return out, lse, tol
