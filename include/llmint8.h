@@ -554,14 +554,20 @@ LLMINT8_API size_t llmint8_kv_attention_workspace_size(int64_t heads, int64_t kv
  *   s_j = scale * q_i . k_j  [+ alibi_slopes[g] * (j - p_i)],
  *   out_i = sum_j softmax(s)_j v_j,   lse_i = log sum_j exp(s_j)
  * with k_j, v_j the cached values. Scores, softmax statistics and sums are
- * held in fp32; the weights enter the value product as fp16. A row that no
- * key is left for gives zeros and lse -inf.
+ * held in fp32; the weights enter the value product as fp16 (off by 2^-11 of
+ * themselves, and by up to 2^-25 of the row's largest where more than 16 rows
+ * share a head, 2^-33 else), or as two fp16 values: see max_new. Values whose
+ * page has an absmax below 1.3e-28 count as with that one. A row that no key is
+ * left for gives zeros and lse -inf.
  *   Q            (device) [tokens x heads x head_dim] of `type`, strides as K
  *   alibi_slopes (device, may be NULL) fp32 [heads]: the linear position
  *                biases BLOOM adds to its scores
  *   max_new      host-side upper bound of the new tokens of any one sequence,
- *                0 if not known. It only chooses among kernels: with a wrong
- *                value the result is the same.
+ *                0 if not known (all tokens of the call then). It chooses among
+ *                kernels, which differ in how the weights are rounded: with
+ *                max_new * heads / cache->heads of at most 8 they keep 22 bits,
+ *                else they are fp16. A wrong value gives right results too,
+ *                but not the same bits; a right one is faster for single tokens.
  *   out          (device) [tokens x heads x head_dim] of `type`, dense
  *   lse          (device, may be NULL) fp32 [tokens x heads]
  *   workspace    (device) >= llmint8_kv_attention_workspace_size bytes, zeroed once

@@ -874,7 +874,8 @@ def kv_attention(Q, k_codes, v_codes, k_absmax, v_absmax, page_table, seq_lens, 
     (kv_append comes first). ``scale`` defaults to head_dim ** -0.5; ``alibi_slopes`` fp32 [heads]
     adds slope * (key position - query position) to the scores; ``lse`` fp32 [tokens x heads]
     receives log sum exp; ``max_new``, an upper bound of the new tokens of one sequence (0:
-    unknown), only helps to choose the kernel (llmint8_kv_attention)."""
+    unknown, all of Q's), chooses the kernel and with it how the weights are rounded; give it
+    where it is known, 1 for a step of single tokens (llmint8_kv_attention)."""
     torch = _torch()
     c, index = _kv_cache(k_codes, v_codes, k_absmax, v_absmax, page_table, seq_lens, cu_rows)
     head_dim = c.head_dim

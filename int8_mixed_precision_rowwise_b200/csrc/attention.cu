@@ -35,7 +35,8 @@ cudaError_t launch_kv_attention(const llmint8_kv_cache &c, const AttnArgs &a, co
     // the kernel that streams the cache once for them, more to the one that
     // fills tensor core tiles of 256. The lengths are on the device, so a batch
     // that may hold both kinds gets both launches, and each takes its own. A
-    // bound that is wrong costs time only: a kernel that is alone takes all.
+    // bound that is wrong costs time, and changes the rounding of the weights: a
+    // kernel that is alone takes all.
     const int64_t most = std::min(a.max_new, a.tokens) * p.group;
     const bool few = most <= kAttnFewRows;
     if (few || c.batch > 1) {

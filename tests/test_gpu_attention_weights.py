@@ -1,5 +1,5 @@
 """GPU checks of how exactly the attention's weights enter the value product: as two fp16 values where at most 8 rows
-share a head (by the bound max_new), as one elsewhere."""
+share a head (by the bound max_new), as one elsewhere; and of what max_new may change."""
 import math
 
 import pytest
@@ -90,3 +90,26 @@ def test_light_keys_beside_a_heavy_one(lib, heads, news):
     lim = tol * 1.01 + ref.abs() * 2.0 ** -11 + 2.0 ** -25
     assert float((lim / ref.abs()).max()) < 0.004  # a quarter of the light keys 3.7% off is 0.009
     check_attention(out, ref, tol, F16)
+
+
+@pytest.mark.parametrize("heads,kv_heads,news", [(8, 2, [1, 1, 1]), (4, 4, [1, 8, 3]), (8, 1, [1, 2, 1]),
+                                                 (16, 2, [1, 20, 2])])
+def test_max_new_changes_no_more_than_the_rounding(lib, heads, kv_heads, news):
+    """Bounds that are right, too high, too low or missing: every result is within the bound of weights in fp16, with
+    tiles of 8 rows (max_new, or else all tokens, times the heads of a group) within that of two fp16 values, and
+    the same call gives the same bits."""
+    g = torch.Generator().manual_seed(heads)
+    lens, total, group = [300, 40, 77], sum(news), heads // kv_heads
+    table, pages = page_table(lens, 16, g, "cuda")
+    bufs = cancelling_cache(pages, kv_heads, 16, 128, g)
+    Q = torch.randn((total, heads, 128), generator=g).to("cuda").half()
+    args = (table, ints(lens), cu(news, "cuda"))
+    for max_new in (0, 1, 2, max(news), 8, 5000):
+        few = min(max_new or total, total) * group <= 8
+        ref, ref_lse, tol = attention_reference(Q, *bufs, table, lens, news, 1e-3,
+                                                **(TWO if few else dict(weight=2.0 ** -11, least=2.0 ** -25)))
+        lse = torch.empty((total, heads), device="cuda")
+        out = lib.kv_attention(Q, *bufs, *args, scale=1e-3, max_new=max_new, lse=lse)
+        check_attention(out, ref, tol, F16)
+        assert bool(((lse - ref_lse).abs() <= 2.0 ** -17 * (1 + ref_lse.abs())).all())
+        assert torch.equal(out, lib.kv_attention(Q, *bufs, *args, scale=1e-3, max_new=max_new))
