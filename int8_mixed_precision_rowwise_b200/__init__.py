@@ -206,8 +206,8 @@ def get_workspace(nbytes: int, device):
 def workspaces(device=None) -> list:
     """The cached workspaces (of one device index, or all). Those that belong to captured graphs are not
     among them (to read the status of replays, give the captured calls a workspace)."""
-    return [ws for cached in (_workspaces, _serving_workspaces) for (idx, _), ws in cached.items()
-            if device is None or idx == device]
+    return [ws for cached in (_workspaces, _serving_workspaces) for key, ws in cached.items()
+            if device is None or key[0] == device]
 
 
 def workspace_init(ws) -> None:
@@ -638,48 +638,54 @@ def _raw_stream(index):
     return get(index) if get else torch.cuda.current_stream(index).cuda_stream
 
 
-# The workspaces of these calls, one per (device index, raw stream handle), of one
-# size that is enough for every shape, so that they never grow. (get_workspace's,
-# which the linears use, do.) Calls that are captured get one of the graph's own,
-# from its memory: a graph may be replayed on any stream, next to calls on the one it
-# was captured on and to other graphs captured there. Per stream the latest capture's
-# is remembered, with the number of that capture.
+# The workspaces of these calls, by (device index, raw stream handle, attention's or
+# not), of two sizes that are enough for every shape, so that they never grow.
+# (get_workspace's, which the linears use, do.) Attention's holds the parked parts, 43
+# MB; the others' has less than 1 MB. Calls that are captured get workspaces of the
+# graph's own, from its memory: a graph may be replayed on any stream, next to calls on
+# the one it was captured on and to other graphs captured there. Per stream the latest
+# capture's are held, with the number of that capture, until the stream is used
+# outside of it: from then on the graph alone keeps their memory.
 _serving_workspaces: dict = {}
 _captured_workspaces: dict = {}
 
 
-def _workspace(workspace, index):
+def _workspace(workspace, index, attention=True):
     """(address, bytes) of the given workspace, or of the one of the device's current stream."""
     if workspace is None:
         stream = _raw_stream(index)
+        key = index, stream, attention
         capture = load()["_stream_capture_id"](stream) if stream else 0  # the default stream is never captured
         if capture:
-            held = _captured_workspaces.get((index, stream))
-            workspace = held[1] if held and held[0] == capture else _new_captured_workspace(index, stream, capture)
+            held = _captured_workspaces.get(key)
+            workspace = held[1] if held and held[0] == capture else _new_captured_workspace(key, capture)
         else:
-            workspace = _serving_workspaces.get((index, stream))
+            if _captured_workspaces:
+                _captured_workspaces.pop((index, stream, True), None)
+                _captured_workspaces.pop((index, stream, False), None)
+            workspace = _serving_workspaces.get(key)
             if workspace is None:
-                workspace = _serving_workspaces[(index, stream)] = _new_serving_workspace(index, True)
+                workspace = _serving_workspaces[key] = _new_serving_workspace(index, attention, True)
     elif workspace.get_device() != index or workspace.dtype is not _torch().uint8 or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous uint8 tensor on cuda:{index}")
     return workspace.data_ptr(), workspace.numel()
 
 
-def _new_serving_workspace(index, cleared):
+def _new_serving_workspace(index, attention, cleared):
     torch = _torch()
     make = torch.zeros if cleared else torch.empty
-    return make(max(kv_attention_workspace_size(1, 1, 128), quantize_workspace_size(0, 133136)), dtype=torch.uint8,
-                device=torch.device("cuda", index))
+    return make(kv_attention_workspace_size(1, 1, 128) if attention else quantize_workspace_size(0, 133136),
+                dtype=torch.uint8, device=torch.device("cuda", index))
 
 
-def _new_captured_workspace(index, stream, capture):
+def _new_captured_workspace(key, capture):
     torch = _torch()
-    _captured_workspaces.pop((index, stream), None)  # its memory may serve again
-    with torch.cuda.device(index):
-        ws = _new_serving_workspace(index, False)
+    _captured_workspaces.pop(key, None)  # its memory may serve again
+    with torch.cuda.device(key[0]):
+        ws = _new_serving_workspace(key[0], key[2], False)
         # Captured like all else: every replay starts with the part cleared whose state calls hand on.
         ws[:quantize_workspace_size(0, 0)].zero_()
-    _captured_workspaces[(index, stream)] = capture, ws
+    _captured_workspaces[key] = capture, ws
     return ws
 
 
@@ -739,7 +745,7 @@ def add_rmsnorm_quantize(X, weight, residual=None, eps: float = 1e-6, threshold:
         residual_out = torch.empty_like(X)
     _call("_add_rmsnorm_quantize", index, X.data_ptr(), _ptr(residual), weight.data_ptr(), kind, rows, cols, eps,
           threshold, _ptr(residual_out), _ptr(Y), codes.data_ptr(), row_absmax.data_ptr(), _ptr(outlier_bitmap),
-          *_workspace(workspace, index))
+          *_workspace(workspace, index, False))
     return codes, row_absmax, outlier_bitmap, Y, (X if residual_out is None else residual_out)
 
 
@@ -839,7 +845,7 @@ def kv_append(K, V, k_codes, v_codes, k_absmax, v_absmax, page_table, seq_lens, 
     if v_kind != kind or V.shape[0] != tokens:
         raise ValueError("K and V must have the same type and shape")
     _call("_kv_append", index, ctypes.byref(c), K.data_ptr(), V.data_ptr(), kind, tokens, k_token, k_head, v_token,
-          v_head, *_workspace(workspace, index))
+          v_head, *_workspace(workspace, index, False))
 
 
 def kv_read(k_codes, v_codes, k_absmax, v_absmax, page_table, seq_lens, cu_rows, tokens: int, dtype=None, K=None,
@@ -859,7 +865,7 @@ def kv_read(k_codes, v_codes, k_absmax, v_absmax, page_table, seq_lens, cu_rows,
     else:
         _need_like(V, "V", dtype, shape, index)
     _call("_kv_read", index, ctypes.byref(c), K.data_ptr(), V.data_ptr(), _value_type(K, "K"), shape[0],
-          *_workspace(workspace, index))
+          *_workspace(workspace, index, False))
     return K, V
 
 
