@@ -40,9 +40,9 @@
 // warp and nothing rescaled for most units.
 //
 // On B200: 64 sequences of 100 to 8000 tokens, 32 heads over 8, pages of 16:
-// 101 us, 5.3 TB/s of the cache (5.8 without the 9 us that a call of any size
-// takes); 16 sequences of up to 2048, 112 heads with position biases: 117 us,
-// 5.0 TB/s; two of 131072 and 100000, 16 rows a head: 98 us, 4.8 TB/s.
+// 100 us, 5.3 TB/s of the cache (5.9 without the 9 us that a call of any size
+// takes); 16 sequences of up to 2048, 112 heads with position biases: 116 us,
+// 5.1 TB/s; two of 131072 and 100000, 16 rows a head: 98 us, 4.8 TB/s.
 #include <cuda.h>
 #include <cuda_runtime.h>
 

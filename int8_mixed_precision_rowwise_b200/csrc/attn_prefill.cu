@@ -21,7 +21,7 @@
 // loads the codes with TMA, one thread issues the products.
 //
 // On B200, chunks of 2048 and 1500 tokens over 8192 and 6000, 32 heads over 8:
-// 430 us, 860 TFLOP/s, 0.51 of the measured bf16 rate. A unit takes about 3950
+// 430 to 440 us, 840 to 860 TFLOP/s, 0.50 to 0.51 of the measured bf16 rate. A unit takes about 3950
 // cycles; the special function unit and the tensor cores are busy for 2048 of
 // them each, the chain scores -> weights (2600 for a row half, with both halves
 // and the codes' conversion sharing the issue slots) -> products decides.

@@ -9,9 +9,11 @@
 //
 // Bound by HBM: per element two 2-byte reads, a 2-byte h, a 2-byte y and a
 // 1-byte code written. On B200, 4001 x 14336 with a residual and outlier
-// columns: 104 us, 4.9 TB/s (a copy runs at 6.5): a row's two reductions and
-// about 200 instructions per 8 columns keep the SMs 42% busy and the loads
-// waiting; 32 x 14336: 8.5 us. The codes' values again: 25 us, 6.9 TB/s.
+// columns: 107 us, 4.8 TB/s (a copy runs at 6.5): a row's two reductions and
+// about 275 instructions per 8 columns (issue slots 53% taken) keep the loads
+// waiting; 32 x 14336: 9 us. The codes' values again: 26 us, 6.7 TB/s. The sum
+// of squares as a pair costs 3% of that (130 -> 133 us both together; 2048 x
+// 4096, codes only, 15.4 -> 16.9); in doubles, reduced by shuffles, 142 and 18.9.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
