@@ -514,8 +514,8 @@ typedef struct llmint8_kv_cache {
  *   S > old; new codes are rint(x * (127 / S)); the absmax becomes S
  * in fp32, keys and values apart (S below 4e-37 gives codes 0). What a page
  * held before its first token was written does not matter: pages need no
- * clearing. A page that receives tokens belongs to one sequence; full pages
- * may be shared.
+ * clearing. A page that receives tokens belongs to one sequence, at one place
+ * of its table; full pages may be shared.
  *   K, V        (device) [tokens x heads x head_dim] of `type`; strides in
  *               elements between tokens and between heads (multiples of 8,
  *               not negative), so that they may be parts of a fused
